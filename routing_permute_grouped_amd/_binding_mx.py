@@ -1,0 +1,382 @@
+"""ctypes binding of the calls include/moe_mx.h declares: 4-bit quantisation and products,
+8-bit checkpoints of fc1's pre-activations. Argument marshalling only, in the manner of
+``_binding``; each call runs on the device of its first tensor (all others must be there)
+and, without ``stream``, on that device's current stream.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _binding as B
+
+_P, _I, _I64, _SZ = B._P, B._I, B._I64, B._SZ
+MX_SIGNATURES = [
+    ("moe_quantize_mxfp4", _I, [_I, _P, _I64, _I, _P, _P, _I, _P]),
+    ("moe_dequantize_mxfp4", _I, [_I, _P, _P, _I64, _I, _I, _P, _P]),
+    ("moe_dequantize_mxfp8", _I, [_I, _P, _P, _I64, _I, _I, _P, _P]),
+    ("moe_permute_mxfp4", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P,
+                               _P, _SZ, _P, _P]),
+    ("moe_grouped_fc1_swiglu_mxfp4", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _P, _P, _P,
+                                          _P, _P, _P, _SZ, _P]),
+    ("moe_grouped_fc2_mxfp4", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _P, _P, _P, _P, _SZ,
+                                   _P]),
+    ("moe_grouped_swiglu_masked_mxfp4", _I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P,
+                                             _P, _P]),
+    ("moe_grouped_fc1_swiglu_ckpt8", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I64, _P, _P, _P, _P,
+                                          _P, _P, _SZ, _P]),
+    ("moe_grouped_dgrad_swiglu_ckpt8", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I64, _P, _P, _P, _P,
+                                            _P, _P, _I, _I, _P, _P, _P, _P, _SZ, _P, _SZ, _P]),
+    ("moe_ckpt8_scratch_bytes", _SZ, [_I, _I64]),
+]
+for _name, _res, _args in MX_SIGNATURES:
+    _fn = getattr(B.lib, _name)
+    _fn.restype, _fn.argtypes = _res, _args
+
+
+def _run(name: str, stream, tensors: dict, args) -> None:
+    """Check that every tensor is contiguous and on the first one's GPU, and call ``name``
+    there; ``args`` maps the pointers by name and the stream to the C arguments."""
+    ptr, dev = {}, None
+    for n, t in tensors.items():
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError(f"{n}: tensor must live on the GPU")
+            if not t.is_contiguous():
+                raise ValueError(f"{n}: tensor must be contiguous")
+            dev = t.device if dev is None else dev
+            if t.device != dev:
+                raise ValueError(f"{n}: on {t.device}, expected {dev}")
+        ptr[n] = None if t is None else t.data_ptr()
+    with torch.cuda.device(dev):
+        B._check(name, getattr(B.lib, name)(*args(ptr, B._stream(stream))))
+
+
+def _scale_bytes(rows: int, C: int) -> int:
+    return rows * (C // 32)
+
+
+def _block_rows(codes: torch.Tensor, name: str, per: int) -> Tuple[int, int]:
+    """(R, C) of code rows [..., C * per / 2]: per 2 for a byte a code, 1 for two a byte."""
+    B._dtype(codes, name, torch.uint8)
+    if codes.dim() < 1 or codes.numel() == 0:
+        raise ValueError(f"{name}: shape {tuple(codes.shape)}, expected rows of codes")
+    width = codes.shape[-1]
+    return codes.numel() // width, width * 2 // per
+
+
+def moe_quantize_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                       scales: Optional[torch.Tensor] = None, layout: int = B.MOE_MX_ROWS,
+                       stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """MXFP4 codes and E8M0 scales of the rows of x [..., C]. Returns (q uint8 [..., C/2], the
+    even element in the low half, and scales): layout MOE_MX_ROWS, uint8 [..., C/32] (C a
+    multiple of 32); MOE_MX_KSTEPS, the products' k-step words as uint8 [C/128, R, 4] (R
+    rows, C a multiple of 128)."""
+    B._layer_dtype(x, "x")
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected rows of values")
+    C = x.shape[-1]
+    R = x.numel() // C
+    B._numel(q, "q", R * C // 2, torch.uint8)
+    B._numel(scales, "scales", _scale_bytes(R, C), torch.uint8)
+    if q is None:
+        q = torch.empty((*x.shape[:-1], C // 2), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        shape = (C // 128, R, 4) if layout == B.MOE_MX_KSTEPS else (*x.shape[:-1], C // 32)
+        scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+    _run("moe_quantize_mxfp4", stream, dict(x=x, q=q, scales=scales), lambda p, s: (
+        B._dt(x), p["x"], R, C, p["q"], p["scales"], layout, s))
+    return q, scales
+
+
+def _dequantize(name: str, per: int, q, scales, out, layout, dtype, stream) -> torch.Tensor:
+    R, C = _block_rows(q, "q", per)
+    B._numel(scales, "scales", _scale_bytes(R, C), torch.uint8)
+    if out is None:
+        if dtype not in B._LAYER_DTYPES:
+            raise TypeError(f"dtype {dtype}, expected float32 or bfloat16")
+        out = torch.empty((*q.shape[:-1], C), dtype=dtype, device=q.device)
+    B._layer_dtype(out, "out")
+    B._numel(out, "out", R * C)
+    _run(name, stream, dict(q=q, scales=scales, out=out), lambda p, s: (
+        B._dt(out), p["q"], p["scales"], R, C, layout, p["out"], s))
+    return out
+
+
+def moe_dequantize_mxfp4(q: torch.Tensor, scales: torch.Tensor,
+                         out: Optional[torch.Tensor] = None, layout: int = B.MOE_MX_ROWS,
+                         dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values [..., C] of MXFP4 codes q [..., C/2] and their scales, in ``dtype`` (or
+    out's)."""
+    return _dequantize("moe_dequantize_mxfp4", 1, q, scales, out, layout, dtype, stream)
+
+
+def moe_dequantize_mxfp8(q: torch.Tensor, scales: torch.Tensor,
+                         out: Optional[torch.Tensor] = None, layout: int = B.MOE_MX_ROWS,
+                         dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values [..., C] of MXFP8 (e4m3) codes q [..., C] and their scales, in ``dtype`` (or
+    out's)."""
+    return _dequantize("moe_dequantize_mxfp8", 2, q, scales, out, layout, dtype, stream)
+
+
+def moe_permute_mxfp4(xq: torch.Tensor, xs: torch.Tensor, topk_idx: torch.Tensor, E: int,
+                      m_tile: int, m_cap: Optional[int] = None, out: Optional[dict] = None,
+                      stream=None) -> dict:
+    """moe_permute for the 4-bit payload xq [T, D/2], xs [T, D/32]: dict with xq_perm
+    [m_cap, D/2], xs_perm (the scales in k-step words, uint8 [D/128, m_cap, 4]) and the
+    metadata. Buffers given in ``out`` are reused."""
+    B._dims(xq, "xq", 2)
+    T, D = _block_rows(xq, "xq", 1)
+    B._numel(xs, "xs", _scale_bytes(T, D), torch.uint8)
+    k = B._check_idx(topk_idx, T)
+    dev = xq.device
+    if m_cap is None:
+        m_cap = B.moe_capacity(T, k, E, m_tile)
+        if m_cap < 0:
+            raise ValueError(f"no capacity for T={T}, k={k}, E={E}, m_tile={m_tile}")
+    o = dict(out or {})
+    B._rows(o.get("xq_perm"), "xq_perm", m_cap, D // 2, torch.uint8)
+    B._numel(o.get("xs_perm"), "xs_perm", (D // 128) * m_cap * 4, torch.uint8)
+    B._check_layout_out(o, T, k, E, m_cap, m_tile)
+    ws = max(4, B.moe_permute_workspace_bytes(T, k, E))
+    B._nbytes(o.get("workspace"), "workspace", ws)
+    i32 = dict(dtype=torch.int32, device=dev)
+    o.setdefault("xq_perm", torch.empty((m_cap, D // 2), dtype=torch.uint8, device=dev))
+    o.setdefault("xs_perm", torch.empty((D // 128, m_cap, 4), dtype=torch.uint8, device=dev))
+    o.setdefault("counts", torch.empty(E, **i32))
+    o.setdefault("offsets", torch.empty(E + 1, **i32))
+    o.setdefault("dst_row", torch.empty((T, k), **i32))
+    o.setdefault("src_row", torch.empty(m_cap, **i32))
+    o.setdefault("tile_expert", torch.empty(m_cap // m_tile, **i32))
+    o.setdefault("dev_err", torch.empty(1, **i32))
+    o.setdefault("workspace", torch.empty(ws, dtype=torch.uint8, device=dev))
+    names = ("xq_perm", "xs_perm", "counts", "offsets", "dst_row", "src_row", "tile_expert",
+             "dev_err", "workspace")
+    wsb = o["workspace"].numel() * o["workspace"].element_size()
+    _run("moe_permute_mxfp4", stream,
+         dict(xq=xq, xs=xs, topk_idx=topk_idx, **{n: o[n] for n in names}), lambda p, s: (
+             p["xq"], p["xs"], p["topk_idx"], T, D, E, k, m_tile, m_cap, p["xq_perm"],
+             p["xs_perm"], p["counts"], p["offsets"], p["dst_row"], p["src_row"],
+             p["tile_expert"], p["workspace"], wsb, p["dev_err"], s))
+    o["m_cap"] = m_cap
+    return o
+
+
+def _mx4_weight(q: torch.Tensor, s: torch.Tensor, name: str, shape=None) -> Tuple[int, int, int]:
+    """(E, N, K) of codes [E, N, K/2] (of ``shape`` [E, N, K], if given) with their k-step
+    words [K/128, E*N, 4]."""
+    B._dtype(q, name + "q", torch.uint8)
+    B._dims(q, name + "q", 3)
+    E, N, K = q.shape[0], q.shape[1], q.shape[2] * 2
+    if shape is not None and (E, N, K) != tuple(shape):
+        raise ValueError(f"{name}q: shape {tuple(q.shape)}, expected "
+                         f"{(shape[0], shape[1], shape[2] // 2)}")
+    B._numel(s, name + "s", (K // 128) * E * N * 4, torch.uint8)
+    return E, N, K
+
+
+def _mx4_rows(q: torch.Tensor, s: torch.Tensor, name: str, m_cap: int, K: int) -> None:
+    B._rows(q, name + "q", m_cap, K // 2, torch.uint8)
+    B._numel(s, name + "s", (K // 128) * m_cap * 4, torch.uint8)
+
+
+def _wsz(ws: Optional[torch.Tensor]) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def moe_grouped_fc1_swiglu_mxfp4(xq_perm: torch.Tensor, xs_perm: torch.Tensor,
+                                 offsets: torch.Tensor, tile_expert: torch.Tensor,
+                                 w1q: torch.Tensor, w1s: torch.Tensor, w3q: torch.Tensor,
+                                 w3s: torch.Tensor, m_tile: int, m_cap: Optional[int] = None,
+                                 h: Optional[torch.Tensor] = None,
+                                 workspace: Optional[torch.Tensor] = None, stream=None,
+                                 counts: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """h [m_cap, F] bf16 = silu(a)*b from 4-bit rows (codes [m_cap, D/2], k-step words
+    [D/128, m_cap, 4]) and 4-bit w1, w3 (codes [E, F, D/2], k-step words [D/128, E*F, 4])."""
+    E, F, D = _mx4_weight(w1q, w1s, "w1")
+    _mx4_weight(w3q, w3s, "w3", (E, F, D))
+    if m_cap is None:
+        m_cap = xq_perm.shape[0]
+    _mx4_rows(xq_perm, xs_perm, "x", m_cap, D)
+    B._check_segments(offsets, tile_expert, E, m_cap, m_tile)
+    B._numel(counts, "counts", E, torch.int32)
+    B._rows(h, "h", m_cap, F, torch.bfloat16)
+    if h is None:
+        h = torch.empty((m_cap, F), dtype=torch.bfloat16, device=xq_perm.device)
+    _run("moe_grouped_fc1_swiglu_mxfp4", stream,
+         dict(xq_perm=xq_perm, xs_perm=xs_perm, offsets=offsets, counts=counts,
+              tile_expert=tile_expert, w1q=w1q, w1s=w1s, w3q=w3q, w3s=w3s, h=h,
+              workspace=workspace), lambda p, s: (
+             p["xq_perm"], p["xs_perm"], p["offsets"], p["counts"], p["tile_expert"], E, D, F,
+             m_tile, m_cap, p["w1q"], p["w1s"], p["w3q"], p["w3s"], p["h"], p["workspace"],
+             _wsz(workspace), s))
+    return h
+
+
+def moe_grouped_fc2_mxfp4(hq: torch.Tensor, hs: torch.Tensor, offsets: torch.Tensor,
+                          tile_expert: torch.Tensor, w2q: torch.Tensor, w2s: torch.Tensor,
+                          m_tile: int, m_cap: Optional[int] = None,
+                          y_perm: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None,
+                          counts: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y_perm [m_cap, D] bf16 = h w2[e]^T from 4-bit rows (codes [m_cap, F/2], k-step words
+    [F/128, m_cap, 4]) and 4-bit w2 (codes [E, D, F/2], k-step words [F/128, E*D, 4])."""
+    E, D, F = _mx4_weight(w2q, w2s, "w2")
+    if m_cap is None:
+        m_cap = hq.shape[0]
+    _mx4_rows(hq, hs, "h", m_cap, F)
+    B._check_segments(offsets, tile_expert, E, m_cap, m_tile)
+    B._numel(counts, "counts", E, torch.int32)
+    B._rows(y_perm, "y_perm", m_cap, D, torch.bfloat16)
+    if y_perm is None:
+        y_perm = torch.empty((m_cap, D), dtype=torch.bfloat16, device=hq.device)
+    _run("moe_grouped_fc2_mxfp4", stream,
+         dict(hq=hq, hs=hs, offsets=offsets, counts=counts, tile_expert=tile_expert, w2q=w2q,
+              w2s=w2s, y_perm=y_perm, workspace=workspace), lambda p, s: (
+             p["hq"], p["hs"], p["offsets"], p["counts"], p["tile_expert"], E, D, F, m_tile,
+             m_cap, p["w2q"], p["w2s"], p["y_perm"], p["workspace"], _wsz(workspace), s))
+    return y_perm
+
+
+def moe_grouped_swiglu_masked_mxfp4(x_masked: torch.Tensor, counts: torch.Tensor,
+                                    w1q: torch.Tensor, w1s: torch.Tensor, w3q: torch.Tensor,
+                                    w3s: torch.Tensor, w2q: torch.Tensor, w2s: torch.Tensor,
+                                    cap: int, h: Optional[torch.Tensor] = None,
+                                    y: Optional[torch.Tensor] = None, stream=None):
+    """(h, y) on the valid rows of every slab of the masked layout, bf16 rows against 4-bit
+    weights (codes and k-step words as moe_grouped_fc1_swiglu_mxfp4 and
+    moe_grouped_fc2_mxfp4 take them); the other rows of h and y are left as they are."""
+    E, F, D = _mx4_weight(w1q, w1s, "w1")
+    _mx4_weight(w3q, w3s, "w3", (E, F, D))
+    _mx4_weight(w2q, w2s, "w2", (E, D, F))
+    B._rows(x_masked, "x_masked", E * cap, D, torch.bfloat16)
+    B._numel(counts, "counts", E, torch.int32)
+    B._rows(h, "h", E * cap, F, torch.bfloat16)
+    B._rows(y, "y", E * cap, D, torch.bfloat16)
+    dev = x_masked.device
+    if h is None:
+        h = torch.empty((E * cap, F), dtype=torch.bfloat16, device=dev)
+    if y is None:
+        y = torch.empty((E * cap, D), dtype=torch.bfloat16, device=dev)
+    _run("moe_grouped_swiglu_masked_mxfp4", stream,
+         dict(x_masked=x_masked, counts=counts, w1q=w1q, w1s=w1s, w3q=w3q, w3s=w3s, w2q=w2q,
+              w2s=w2s, h=h, y=y), lambda p, s: (
+             p["x_masked"], p["counts"], E, D, F, cap, p["w1q"], p["w1s"], p["w3q"], p["w3s"],
+             p["w2q"], p["w2s"], p["h"], p["y"], s))
+    return h, y
+
+
+def moe_grouped_fc1_swiglu_ckpt8(x_perm: torch.Tensor, offsets: torch.Tensor,
+                                 tile_expert: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor,
+                                 m_tile: int, m_cap: Optional[int] = None,
+                                 h: Optional[torch.Tensor] = None,
+                                 ab_codes: Optional[torch.Tensor] = None,
+                                 ab_scales: Optional[torch.Tensor] = None,
+                                 workspace: Optional[torch.Tensor] = None, stream=None,
+                                 rows_used: Optional[int] = None,
+                                 counts: Optional[torch.Tensor] = None):
+    """moe_grouped_fc1_swiglu (bf16) that keeps the pre-activations [a | b] for the backward as
+    MXFP8. Returns (h [m_cap, F], ab_codes uint8 [m_cap, 2F], ab_scales uint8
+    [m_cap, 2F/32])."""
+    B._dims(w1, "w1", 3)
+    E, F, D = w1.shape
+    B._weights(w1, w3, None, torch.bfloat16, E, F, D)
+    if m_cap is None:
+        m_cap = x_perm.shape[0]
+    B._rows(x_perm, "x_perm", B._used(rows_used, m_cap), D, torch.bfloat16)
+    B._check_segments(offsets, tile_expert, E, m_cap, m_tile)
+    B._numel(counts, "counts", E, torch.int32)
+    B._rows(h, "h", m_cap, F, torch.bfloat16)
+    B._rows(ab_codes, "ab_codes", m_cap, 2 * F, torch.uint8)
+    B._rows(ab_scales, "ab_scales", m_cap, F // 16, torch.uint8)
+    dev = x_perm.device
+    if h is None:
+        h = torch.empty((m_cap, F), dtype=torch.bfloat16, device=dev)
+    if ab_codes is None:
+        ab_codes = torch.empty((m_cap, 2 * F), dtype=torch.uint8, device=dev)
+    if ab_scales is None:
+        ab_scales = torch.empty((m_cap, F // 16), dtype=torch.uint8, device=dev)
+    _run("moe_grouped_fc1_swiglu_ckpt8", stream,
+         dict(x_perm=x_perm, offsets=offsets, counts=counts, tile_expert=tile_expert, w1=w1,
+              w3=w3, h=h, ab_codes=ab_codes, ab_scales=ab_scales, workspace=workspace),
+         lambda p, s: (
+             p["x_perm"], p["offsets"], p["counts"], p["tile_expert"], E, D, F, m_tile, m_cap,
+             p["w1"], p["w3"], p["h"], p["ab_codes"], p["ab_scales"], p["workspace"],
+             _wsz(workspace), s))
+    return h, ab_codes, ab_scales
+
+
+def moe_ckpt8_scratch_bytes(F: int, m_cap: int) -> int:
+    return int(B.lib.moe_ckpt8_scratch_bytes(F, m_cap))
+
+
+def moe_grouped_dgrad_swiglu_ckpt8(dout_perm: torch.Tensor, offsets: torch.Tensor,
+                                   tile_expert: torch.Tensor, w2: torch.Tensor,
+                                   ab_codes: torch.Tensor, ab_scales: torch.Tensor, m_tile: int,
+                                   m_cap: Optional[int] = None,
+                                   src_row: Optional[torch.Tensor] = None,
+                                   dst_row: Optional[torch.Tensor] = None,
+                                   topk_w: Optional[torch.Tensor] = None,
+                                   dab: Optional[torch.Tensor] = None,
+                                   hw: Optional[torch.Tensor] = None,
+                                   dtopk_w: Optional[torch.Tensor] = None,
+                                   scratch: Optional[torch.Tensor] = None,
+                                   workspace: Optional[torch.Tensor] = None, stream=None,
+                                   rows_used: Optional[int] = None,
+                                   counts: Optional[torch.Tensor] = None):
+    """The backward of combine, fc2 and silu(a)*b from an 8-bit checkpoint, for the output
+    gradient's rows dout_perm [m_cap, D] (moe_permute of dout, unweighted). Returns
+    (dab [m_cap, 2F], hw [m_cap, F], dtopk_w [T, k] float32): dab for moe_grouped_dgrad_fc1
+    and the wgrad of w1 and w3, hw = w*silu(a)*b for the wgrad of w2 (dW2 = dout_perm^T hw).
+    Without ``topk_w`` every row's weight is 1 and dtopk_w is None (``src_row``, ``dst_row``
+    and ``scratch`` are then not used); with it, ``src_row`` and ``dst_row`` are needed."""
+    B._dims(w2, "w2", 3)
+    E, D, F = w2.shape
+    B._weights(None, None, w2, torch.bfloat16, E, F, D)
+    if m_cap is None:
+        m_cap = dout_perm.shape[0]
+    ru = B._used(rows_used, m_cap)
+    B._rows(dout_perm, "dout_perm", ru, D, torch.bfloat16)
+    B._check_segments(offsets, tile_expert, E, m_cap, m_tile)
+    B._numel(counts, "counts", E, torch.int32)
+    B._rows(ab_codes, "ab_codes", ru, 2 * F, torch.uint8)
+    B._rows(ab_scales, "ab_scales", ru, F // 16, torch.uint8)
+    B._rows(dab, "dab", m_cap, 2 * F, torch.bfloat16)
+    B._rows(hw, "hw", m_cap, F, torch.bfloat16)
+    dev = dout_perm.device
+    T = k = need = 0
+    if topk_w is not None:
+        B._dims(topk_w, "topk_w", 2)
+        B._dtype(topk_w, "topk_w", torch.float32)
+        T, k = topk_w.shape
+        if src_row is None or dst_row is None:
+            raise ValueError("topk_w needs src_row and dst_row")
+        B._numel(src_row, "src_row", m_cap, torch.int32)
+        B._exact(dst_row, "dst_row", (T, k), torch.int32)
+        B._exact(dtopk_w, "dtopk_w", (T, k), torch.float32)
+        need = moe_ckpt8_scratch_bytes(F, m_cap)
+        B._nbytes(scratch, "scratch", need)
+    elif dtopk_w is not None:
+        raise ValueError("dtopk_w needs topk_w")
+    if dab is None:
+        dab = torch.empty((m_cap, 2 * F), dtype=torch.bfloat16, device=dev)
+    if hw is None:
+        hw = torch.empty((m_cap, F), dtype=torch.bfloat16, device=dev)
+    if topk_w is None:
+        src_row = dst_row = scratch = None
+    else:
+        if dtopk_w is None:
+            dtopk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        if scratch is None:
+            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+    _run("moe_grouped_dgrad_swiglu_ckpt8", stream,
+         dict(dout_perm=dout_perm, offsets=offsets, counts=counts, tile_expert=tile_expert,
+              w2=w2, ab_codes=ab_codes, ab_scales=ab_scales, src_row=src_row, dst_row=dst_row,
+              topk_w=topk_w, dab=dab, hw=hw, dtopk_w=dtopk_w, scratch=scratch,
+              workspace=workspace), lambda p, s: (
+             p["dout_perm"], p["offsets"], p["counts"], p["tile_expert"], E, D, F, m_tile, m_cap,
+             p["w2"], p["ab_codes"], p["ab_scales"], p["src_row"], p["dst_row"], p["topk_w"], T,
+             k, p["dab"], p["hw"], p["dtopk_w"], p["scratch"], _wsz(scratch), p["workspace"],
+             _wsz(workspace), s))
+    return dab, hw, dtopk_w

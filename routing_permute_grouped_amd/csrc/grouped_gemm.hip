@@ -88,14 +88,128 @@ __device__ __forceinline__ void store4(bf16_t* p, float a, float b, float c, flo
 //          dh itself -> `dh` [m][N] when set
 // (the backward of the activation, "Expert Parallelism (EP)", section 5: the fc of the
 // forward mirrors into an m-grouped dgrad).
-enum Mode { kFc1 = 0, kFc2 = 1, kDgrad = 2 };
+//   kFc1Q  as kFc1, with [a | b] kept as e4m3 codes q [m][2N] and E8M0 scales
+//          qs [m][2N/32], quantised from the float32 sums
+//   kDgradQ  the sums are u = dout w2[e] of the unweighted output gradient; with (a, b)
+//          from such a checkpoint and the row's weight w (rw [m], null: 1):
+//          [w*u*b*silu'(a) | w*u*silu(a)] -> C [m][2N], w*silu(a)*b -> dh [m][N], and the
+//          row's sums of u*silu(a)*b over each 64 columns -> dots [N/64][m_cap] when set
+enum Mode { kFc1 = 0, kFc2 = 1, kDgrad = 2, kFc1Q = 3, kDgradQ = 4 };
+constexpr bool is_fc1(int mode) { return mode == kFc1 || mode == kFc1Q; }
 
 struct Epi {
   bf16_t* C;
   bf16_t* ab;
   bf16_t* dh;
   int N;   // output columns (fc1, dgrad: F; fc2: D)
+  uint8_t* q;
+  uint8_t* qs;
+  const float* rw;
+  float* dots;
+  int m_cap;
 };
+
+// ---- The 8-bit checkpoint of [a | b] --------------------------------------------------
+// MX blocks of 32 columns, the FP8 payload's rule: X is the smallest integer >= -127 with
+// max|v| <= 448 * 2^X, the byte X + 127; e4m3 codes of v / 2^X to nearest even by the
+// hardware's scaled conversion. A block with an infinity or a NaN: byte 255 and zero codes.
+// In the accumulators a block is one 32x32 result's row: lane l and lane l ^ 32 hold 16
+// columns each, in groups of four (8*g + 4*(l / 32) + i), so the block's maximum is one
+// exchange away and nothing passes through LDS.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+// The E8M0 byte of a block whose largest magnitude has the float bits u (integer order, so
+// a NaN counts as largest).
+__device__ __forceinline__ uint32_t mx8_scale_byte(uint32_t u) {
+  const int e = (int)(u >> 23);
+  return e == 255 ? 255u : (uint32_t)max(0, e - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0));
+}
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Codes of four values under the block's scale byte.
+__device__ __forceinline__ uint32_t mx8_codes4(float a, float b, float c, float d, uint32_t sb) {
+  const float s = __uint_as_float(sb << 23);
+  i16x2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, s, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, s, true);
+  return sb == 255u ? 0u : __builtin_bit_cast(uint32_t, w);
+}
+
+// Values of four codes (NaN under byte 255).
+__device__ __forceinline__ void mx8_values4(uint32_t w, uint32_t sb, float (&v)[4]) {
+  const float s = __uint_as_float(sb == 255u ? 0x7fc00000u : sb << 23);
+  const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, false);
+  const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, true);
+  v[0] = lo[0]; v[1] = lo[1]; v[2] = hi[0]; v[3] = hi[1];
+}
+
+// Words of the groups g = 0..3 of a block row (columns 8*g + 4*half ..) to the words of
+// columns 16*half + 4*j, j = 0..3, and back: whole 16-column runs for the memory side.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = (uint32_t)r[0];
+  b = (uint32_t)r[1];
+}
+__device__ __forceinline__ void groups_to_run(uint32_t (&w)[4]) {
+  swap_halves(w[0], w[2]);
+  swap_halves(w[1], w[3]);
+  const uint32_t t = w[1];   // w: columns 0, 8, 4, 12 of the run
+  w[1] = w[2];
+  w[2] = t;
+}
+__device__ __forceinline__ void run_to_groups(uint32_t (&w)[4]) {
+  const uint32_t t = w[1];
+  w[1] = w[2];
+  w[2] = t;
+  swap_halves(w[0], w[2]);
+  swap_halves(w[1], w[3]);
+}
+
+// The lane's 16 values of a block row (by groups), rounded to bf16, to 32 bytes at p: its
+// run. Every lane takes part in the exchange; `writes` lanes store.
+__device__ __forceinline__ void run16_out(bf16_t* p, const float (&v)[16], bool writes) {
+  uint32_t lo[4], hi[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    lo[g] = pack_bf16x2(v[4 * g], v[4 * g + 1]);
+    hi[g] = pack_bf16x2(v[4 * g + 2], v[4 * g + 3]);
+  }
+  groups_to_run(lo);
+  groups_to_run(hi);
+  if (!writes) return;
+  st16(p, u32x4{lo[0], hi[0], lo[1], hi[1]});
+  st16(p + 8, u32x4{lo[2], hi[2], lo[3], hi[3]});
+}
+
+// The lane's 16 sums of one block row, quantised: the run's codes and, from the lanes that
+// write it, the block's byte.
+__device__ __forceinline__ void quantize_run16(const f32x16& v, uint8_t* codes, uint8_t* scale,
+                                               bool writes_scale, bool writes) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+  const uint32_t sb = mx8_scale_byte(m);
+  uint32_t w[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    w[g] = mx8_codes4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3], sb);
+  groups_to_run(w);
+  if (!writes) return;
+  st16(codes, u32x4{w[0], w[1], w[2], w[3]});
+  if (writes_scale) *scale = (uint8_t)sb;
+}
+
+// kDgradQ of one element: u the sum, a and b the checkpoint's values, w the row's weight.
+struct DgradQ {
+  float da, db, hw, dot;
+};
+__device__ __forceinline__ DgradQ dgradq(float u, float a, float b, float w) {
+  const float s = sigmoid(a);
+  const float si = a * s, h = si * b, wu = w * u;
+  return DgradQ{wu * b * (s * (1.0f + a * (1.0f - s))), wu * si, w * h, u * h};
+}
 
 // kDgrad for columns n..n+3 of the row starting at element `row` (m * N): v holds the dh
 // sums, pa and pb the packed bf16 a and b of those columns.
@@ -551,6 +665,90 @@ __device__ __forceinline__ void fc2_epilogue(char* lo, char* hi, const Tile& t, 
   }
 }
 
+// kFc1Q epilogue, straight from the accumulators: the wave's w1 and w3 sums of 32 columns
+// are one MX block each of [a | b] per row.
+template <bool HALF>
+__device__ __forceinline__ void fc1q_epilogue(const Tile& t, const Epi& ep,
+                                              const f32x16 (&acc)[HALF ? 2 : 4][2]) {
+  constexpr int WM = HALF ? 2 : 4;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = threadIdx.x >> 6;
+  const int n = t.n0 + (wave >> 1) * 32;
+  if (n >= ep.N) return;   // N is a multiple of 64: a block of 32 columns is in or out
+#pragma unroll
+  for (int mb = 0; mb < WM; ++mb) {
+    const int r = (wave & 1) * (HALF ? 64 : 128) + mb * 32 + (lane & 31);
+    const bool in = r < t.rows;
+    const size_t row = (size_t)(t.m0 + r) * ep.N;
+    const f32x16 &a = acc[mb][0], &b = acc[mb][1];
+    uint8_t* qs = ep.qs + row / 16 + n / 32;   // 2N/32 bytes a row
+    quantize_run16(a, ep.q + 2 * row + n + 16 * half, qs, half == 0, in);
+    quantize_run16(b, ep.q + 2 * row + ep.N + n + 16 * half, qs + ep.N / 32, half == 1, in);
+    float h[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = silu_mul(a[i], b[i]);
+    run16_out(ep.C + row + n + 16 * half, h, in);
+  }
+}
+
+// kDgradQ epilogue, straight from the accumulators: per row, the wave's two blocks of 32
+// columns with their codes (16 bytes of a and of b a lane) and scales. The products of a
+// row's 64 columns are summed in the lane, then over the two lane halves.
+template <bool HALF>
+__device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep,
+                                                const f32x16 (&acc)[HALF ? 2 : 4][2]) {
+  constexpr int WM = HALF ? 2 : 4;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = threadIdx.x >> 6;
+  const int n0 = t.n0 + (wave >> 1) * 64;
+  const int N = ep.N;
+  if (n0 >= N) return;   // N is a multiple of 64
+#pragma unroll
+  for (int mb = 0; mb < WM; ++mb) {
+    const int r = (wave & 1) * (HALF ? 64 : 128) + mb * 32 + (lane & 31);
+    const bool in = r < t.rows, tok = r < t.vrows;
+    const int m = t.m0 + r;
+    const size_t row = (size_t)m * N;
+    const float w = !tok ? 0.0f : ep.rw ? ep.rw[m] : 1.0f;
+    float dot = 0.0f;
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) {
+      const int n = n0 + 32 * nb;
+      u32x4 ca = {0u, 0u, 0u, 0u}, cb = {0u, 0u, 0u, 0u};
+      uint32_t sa = 0u, sb = 0u;   // pad rows: a = b = 0 and u = 0 give zeros
+      if (tok) {
+        ca = ld16(ep.q + 2 * row + n + 16 * half);
+        cb = ld16(ep.q + 2 * row + N + n + 16 * half);
+        sa = ep.qs[row / 16 + n / 32];
+        sb = ep.qs[row / 16 + N / 32 + n / 32];
+      }
+      uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+      run_to_groups(wa);
+      run_to_groups(wb);
+      float da[16], db[16], hw[16];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float a[4], b[4];
+        mx8_values4(wa[g], sa, a);
+        mx8_values4(wb[g], sb, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const DgradQ d = dgradq(acc[mb][nb][4 * g + i], a[i], b[i], w);
+          da[4 * g + i] = d.da;
+          db[4 * g + i] = d.db;
+          hw[4 * g + i] = d.hw;
+          dot += d.dot;
+        }
+      }
+      run16_out(ep.C + 2 * row + n + 16 * half, da, in);
+      run16_out(ep.C + 2 * row + N + n + 16 * half, db, in);
+      run16_out(ep.dh + row + n + 16 * half, hw, in);
+    }
+    dot += __shfl_xor(dot, 32);
+    if (ep.dots && in && half == 0) ep.dots[(size_t)(n0 >> 6) * ep.m_cap + m] = dot;
+  }
+}
+
 // The end of a tile: the raw float32 sums of a split-K share (`part`, row-major
 // [BM][BP]) or the MODE epilogue. Lane l holds column m = l % 32 of every 32x32 block
 // and panel rows 8*g + 4*(l / 32) + i (i = 0..3) for g = 0..3.
@@ -591,6 +789,14 @@ __device__ __forceinline__ void finish_tile(char* smem, const Tile& t, const Epi
   if (MODE == kFc2) {
     char* st = smem + ((stage0 + ke - kb - 1) & 1) * STAGE_BYTES;
     fc2_epilogue<HALF>(elo ? elo : st, ehi ? ehi : st + A_BYTES, t, ep, acc);
+    return;
+  }
+  if (MODE == kFc1Q) {
+    fc1q_epilogue<HALF>(t, ep, acc);
+    return;
+  }
+  if (MODE == kDgradQ) {
+    dgradq_epilogue<HALF>(t, ep, acc);
     return;
   }
 #pragma unroll
@@ -839,6 +1045,178 @@ __device__ __forceinline__ void run_tile_mx(char* smem, const Tile& t, const Epi
   finish_tile<kFc1, HALF>(smem, t, ep, kb, ke, part, stage0, acc);
 }
 
+// ---------------------------------------------------------------------------
+// MXFP4 products: activations and weights in OCP E2M1 (two codes a byte, the even k in
+// the low half) with one E8M0 scale per 32 values along K, on
+// v_mfma_scale_f32_32x32x64_f8f6f4 with both operands FP4 (four operand registers and
+// half the FP8 cycles). A k-step is 256 k: 128-byte LDS rows again, so the stages, the
+// swizzle, the load pattern and the epilogues are the bf16 kernel's, and per byte moved
+// the matrix cores do what they do there. Lane half h of slice ks reads chunk 2*ks + h of
+// its row, 32 codes that are exactly one MX block, with that block's scale byte. K is a
+// multiple of 128; with an odd number of 128-value words the last step runs two slices,
+// and what its loads brought from past the row's end (the next row, or zeros) is not read.
+// ---------------------------------------------------------------------------
+
+// Raw scale words of step kt for this wave: lane half h holds word 2*kt + h of its row
+// (the last word again where the row has none). Rows past the token rows get zero words:
+// their codes are zeros, and a zero word cannot turn those into NaN.
+template <bool FC1, bool HALF>
+__device__ __forceinline__ void mx4_scale_words(const Tile& t, const MxScales& ms, int E, int N,
+                                                int nkw, int kt, uint32_t (&sa)[HALF ? 2 : 4],
+                                                uint32_t (&sw)[2]) {
+  constexpr int WM = HALF ? 2 : 4;
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int arow0 = (wave & 1) * (HALF ? 64 : 128);
+  const int prow0 = (wave >> 1) * 64;
+  const int fr = lane & 31;
+  const int s = min(2 * kt + (lane >> 5), nkw - 1);
+  const uint32_t* a = ms.a + (size_t)s * ms.ra + t.m0;
+#pragma unroll
+  for (int mb = 0; mb < WM; ++mb) {
+    const int r = arow0 + mb * 32 + fr;
+    sa[mb] = r < t.vrows ? a[r] : 0u;
+  }
+  const size_t w0 = (size_t)s * E * N + (size_t)t.e * N;
+  if (FC1) {   // the wave's panel blocks are the w1 and w3 rows of the same columns
+    const size_t r = w0 + min(t.n0 + prow0 / 2 + fr, N - 1);
+    sw[0] = ms.w1[r];
+    sw[1] = ms.w3[r];
+  } else {
+    sw[0] = ms.w1[w0 + min(t.n0 + prow0 + fr, N - 1)];
+    sw[1] = ms.w1[w0 + min(t.n0 + prow0 + 32 + fr, N - 1)];
+  }
+}
+
+// Raw words to the two the MFMAs take: word j of the step in every lane, its bytes moved
+// down by the lane half, so that op_sel byte 0 (even slice) or 2 (odd slice) is the byte
+// of the half's own block.
+__device__ __forceinline__ void mx4_spread(uint32_t raw, uint32_t (&w)[2]) {
+  const auto r = __builtin_amdgcn_permlane32_swap(raw, raw, false, false);
+  const int sh = 8 * ((threadIdx.x & 63) >> 5);
+  w[0] = (uint32_t)r[0] >> sh;
+  w[1] = (uint32_t)r[1] >> sh;
+}
+
+struct Mx4Src {
+  const bf16_t* A;
+  const bf16_t* W1;
+  const bf16_t* W3;
+  int KB, N;   // bytes of a row (K / 2), panel rows of an expert
+  template <bool FC1>
+  __device__ TileLoads loads(const Tile& t) const {
+    return tile_loads<FC1, false, 1>(t, A, W1, W3, KB, N, KB);
+  }
+};
+
+// The bf16 main loop's pipeline on 256-value steps (see mainloop and, for the scale words
+// that run one step ahead, mainloop_mx). nkw: 128-value words of a row.
+template <bool FC1, bool HALF, bool GUARD>
+__device__ __forceinline__ void mainloop_mx4(char* smem, const TileLoads& ld, int kb, int ke,
+                                             int stage0, bool primed, const Tile& nt,
+                                             const Mx4Src& src, bool has_next, int nkb,
+                                             const Tile& t, const MxScales& ms, int E, int nkw,
+                                             f32x16 (&acc)[HALF ? 2 : 4][2]) {
+  constexpr int WM = HALF ? 2 : 4;
+  constexpr int WN = 2;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int arow0 = (wave & 1) * (HALF ? 64 : 128);
+  const int prow0 = (wave >> 1) * 64;
+  const int fr = lane & 31;
+  const uint32_t lds0 = lds_addr(smem) + wave * 1024;
+  const int nmb = GUARD ? max(0, min(WM, (t.vrows - arow0 + 31) >> 5)) : WM;
+#pragma unroll
+  for (int i = 0; i < WM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  if (!primed) {
+    issue_loads(ld, lds0 + stage0 * STAGE_BYTES, kb, 0);
+    issue_loads(ld, lds0 + stage0 * STAGE_BYTES, kb, 1);
+  }
+  uint32_t na[WM], nw[WN];
+  mx4_scale_words<FC1, HALF>(t, ms, E, src.N, nkw, kb, na, nw);
+  auto step = [&](int kt, auto issue) {
+    const int cur = (stage0 + kt - kb) & 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // taken here, where every load has landed: a later use would make the compiler wait
+    // for these words behind the next stage's copies
+    uint32_t sa[WM][2], sw[WN][2];
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+      mx4_spread(na[i], sa[i]);
+      asm volatile("" ::"v"(sa[i][0]), "v"(sa[i][1]));
+    }
+#pragma unroll
+    for (int i = 0; i < WN; ++i) {
+      mx4_spread(nw[i], sw[i]);
+      asm volatile("" ::"v"(sw[i][0]), "v"(sw[i][1]));
+    }
+    if (kt + 1 < ke) mx4_scale_words<FC1, HALF>(t, ms, E, src.N, nkw, kt + 1, na, nw);
+    const char* sA = smem + cur * STAGE_BYTES;
+    const char* sB = sA + A_BYTES;
+    const uint32_t lnext = lds0 + (cur ^ 1) * STAGE_BYTES;
+    uint4 wf[2][WN], af[2][WM];
+    auto frag = [&](int ks, int buf) {
+      const int chk = ks * 2 + (lane >> 5);
+#pragma unroll
+      for (int nb = 0; nb < WN; ++nb)
+        wf[buf][nb] = *reinterpret_cast<const uint4*>(sB + swz(prow0 + nb * 32 + fr, chk));
+#pragma unroll
+      for (int mb = 0; mb < WM; ++mb)
+        af[buf][mb] = *reinterpret_cast<const uint4*>(sA + swz(arow0 + mb * 32 + fr, chk));
+    };
+    auto op = [](const uint4& v) {
+      return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+    };
+    const bool two = 2 * kt + 1 >= nkw;   // the row's last word: two slices
+    frag(0, 0);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      if (ks == 2 && two) break;
+      if (ks < 2) issue(lnext, ks);
+      if (ks + 1 < 4) frag(ks + 1, (ks + 1) & 1);
+#pragma unroll
+      for (int mb = 0; mb < WM; ++mb) {
+        if (GUARD && mb >= nmb) continue;
+#pragma unroll
+        for (int nb = 0; nb < WN; ++nb)
+          acc[mb][nb] = (ks & 1)
+              ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    op(wf[ks & 1][nb]), op(af[ks & 1][mb]), acc[mb][nb], 4, 4, 2,
+                    (int)sw[nb][ks >> 1], 2, (int)sa[mb][ks >> 1])
+              : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    op(wf[ks & 1][nb]), op(af[ks & 1][mb]), acc[mb][nb], 4, 4, 0,
+                    (int)sw[nb][ks >> 1], 0, (int)sa[mb][ks >> 1]);
+      }
+    }
+  };
+  int kt = kb;
+  for (; kt + 1 < ke; ++kt)
+    step(kt, [&](uint32_t l, int ks) { issue_loads<HALF ? 2 : 4>(ld, l, kt + 1, ks); });
+  const TileLoads nxt = src.template loads<FC1>(nt);   // nt is this tile without a next one
+  step(kt, [&](uint32_t l, int ks) {
+    if (has_next) issue_loads(nxt, l, nkb, ks);
+  });
+}
+
+template <int MODE, bool HALF, bool GUARD>
+__device__ __forceinline__ void run_tile_mx4(char* smem, const Tile& t, const Epi& ep, int kb,
+                                             int ke, float* __restrict__ part, int stage0,
+                                             bool primed, const Tile& nt, bool has_next, int nkb,
+                                             const Mx4Src& src, const MxScales& ms, int E,
+                                             int nkw) {
+  f32x16 acc[HALF ? 2 : 4][2];
+  const TileLoads ld = src.template loads<MODE == kFc1>(t);
+  mainloop_mx4<MODE == kFc1, HALF, GUARD>(smem, ld, kb, ke, stage0, primed, nt, src, has_next,
+                                          nkb, t, ms, E, nkw, acc);
+  finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc);
+}
+
 // The rows of each expert: contiguous segments [offsets[e], offsets[e+1]) (cap = 0), of
 // which the first counts[e] hold tokens and the rest are zero pad rows (counts may be
 // null: then every row is treated as a token row), or the masked layout's slabs, rows
@@ -968,7 +1346,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_bf16_kernel(
     const bf16_t* __restrict__ A, Segs sg, int E, int K, int N,
     int m_cap, const bf16_t* __restrict__ W1, const bf16_t* __restrict__ W3, int ksplit,
     Epi ep, float* __restrict__ ws, int slots, MxScales ms) {
-  constexpr bool FC1 = MODE == kFc1;
+  constexpr bool FC1 = is_fc1(MODE);
   constexpr int EB = MX ? 1 : 2;
   __shared__ __attribute__((aligned(16))) char smem[2 * STAGE_BYTES];
   __shared__ Sched sc;
@@ -1060,6 +1438,82 @@ __global__ __launch_bounds__(NTHR, 1) void gg_bf16_kernel(
     primed = has_next;
     cur = nw;
     ld = nl;
+  }
+}
+
+// fc1 (kFc1) or fc2 (kFc2) on MXFP4 rows and weights: the schedule of gg_bf16_kernel over
+// 256-value k-steps. KB: bytes of a row's codes.
+template <int MODE>
+__global__ __launch_bounds__(NTHR, 1) void gg_mx4_kernel(const bf16_t* __restrict__ A, Segs sg,
+                                                         int E, int KB, int N, int m_cap,
+                                                         const bf16_t* __restrict__ W1,
+                                                         const bf16_t* __restrict__ W3, Epi ep,
+                                                         float* __restrict__ ws, int slots,
+                                                         MxScales ms) {
+  constexpr bool FC1 = is_fc1(MODE);
+  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE_BYTES];
+  __shared__ Sched sc;
+  build_sched(sc, sg, E, m_cap);
+
+  const int cols = FC1 ? BP / 2 : BP;
+  const int n_nt = (N + cols - 1) / cols;
+  const int total = sc.tstart[E] * n_nt;
+  const int nk = (KB + 127) / 128;
+  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk);
+  const int items = sp.full + sp.tail * sp.S;
+  int vb = blockIdx.x;
+  if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
+
+  struct Work {
+    Tile t;
+    int kb, ke;
+    float* part;
+  };
+  auto work = [&](int w) {
+    Work r;
+    int tile = w;
+    r.kb = 0;
+    r.ke = nk;
+    r.part = nullptr;
+    if (w >= sp.full) {
+      const int j = w - sp.full, sh = j / sp.tail, i = j - sh * sp.tail;
+      tile = sp.full + i;
+      r.kb = sh * sp.nks;
+      r.ke = min(nk, r.kb + sp.nks);
+      r.part = ws + (size_t)j * (BM * BP);
+    }
+    r.t = decode_item(sc, E, n_nt, cols, tile);
+    return r;
+  };
+
+  if (vb >= items) return;
+  const Mx4Src src{A, W1, W3, KB, N};
+  const int nkw = KB / 64;
+  Work cur = work(vb);
+  int stage0 = 0;
+  bool primed = false;
+  for (int w = vb; w < items; w += gridDim.x) {
+    const bool has_next = w + (int)gridDim.x < items;
+    const Work nw = has_next ? work(w + gridDim.x) : cur;
+    const bool guard = cur.t.vrows < cur.t.rows;
+    if (cur.t.rows > BM / 2) {
+      if (guard)
+        run_tile_mx4<MODE, false, true>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, stage0, primed,
+                                        nw.t, has_next, nw.kb, src, ms, E, nkw);
+      else
+        run_tile_mx4<MODE, false, false>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, stage0,
+                                         primed, nw.t, has_next, nw.kb, src, ms, E, nkw);
+    } else {
+      if (guard)
+        run_tile_mx4<MODE, true, true>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, stage0, primed,
+                                       nw.t, has_next, nw.kb, src, ms, E, nkw);
+      else
+        run_tile_mx4<MODE, true, false>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, stage0,
+                                        primed, nw.t, has_next, nw.kb, src, ms, E, nkw);
+    }
+    stage0 = (stage0 + cur.ke - cur.kb) & 1;
+    primed = has_next;
+    cur = nw;
   }
 }
 
@@ -1228,8 +1682,8 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
     const bf16_t* __restrict__ A, Segs sg, int E, int K, int N, int m_cap,
     const bf16_t* __restrict__ W1, const bf16_t* __restrict__ W3, Epi ep,
     float* __restrict__ ws, int slots) {
-  static_assert(MODE == kFc1 || MODE == kFc2, "the ring serves the forward GEMMs");
-  constexpr bool FC1 = MODE == kFc1;
+  static_assert(is_fc1(MODE) || MODE == kFc2, "the ring serves the forward GEMMs");
+  constexpr bool FC1 = is_fc1(MODE);
   __shared__ __attribute__((aligned(16))) char smem[RING_BYTES];
   int nblk;
   const SchedR sr = build_sched_r(sg, E, m_cap, nblk);
@@ -1313,7 +1767,7 @@ template <int MODE>
 __global__ __launch_bounds__(256) void gg_tail_reduce(Segs sg, int E, int K, int m_cap, int G,
                                                       int slots, const float* __restrict__ ws,
                                                       Epi ep) {
-  constexpr bool FC1 = MODE == kFc1;
+  constexpr bool FC1 = is_fc1(MODE);
   __shared__ Sched sc;
   build_sched(sc, sg, E, m_cap);
   const int N = ep.N;
@@ -1346,7 +1800,56 @@ __global__ __launch_bounds__(256) void gg_tail_reduce(Segs sg, int E, int K, int
     }
     const int n = t.n0 + fl;
     if (n >= N) continue;
-    if (MODE == kDgrad && r >= t.vrows) {   // pad row: zeros, its [a | b] is never read
+    if (MODE == kFc1Q) {   // 8 consecutive lanes hold a block's 32 columns
+      uint32_t ma = 0, mb = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ma = max(ma, abs_bits(a[i]));
+        mb = max(mb, abs_bits(b[i]));
+      }
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) {
+        ma = max(ma, (uint32_t)__shfl_xor((int)ma, d));
+        mb = max(mb, (uint32_t)__shfl_xor((int)mb, d));
+      }
+      const uint32_t sa = mx8_scale_byte(ma), sb = mx8_scale_byte(mb);
+      const size_t row = (size_t)(t.m0 + r) * N;
+      *reinterpret_cast<uint32_t*>(ep.q + 2 * row + n) = mx8_codes4(a[0], a[1], a[2], a[3], sa);
+      *reinterpret_cast<uint32_t*>(ep.q + 2 * row + N + n) =
+          mx8_codes4(b[0], b[1], b[2], b[3], sb);
+      if ((n & 31) == 0) {
+        ep.qs[row / 16 + n / 32] = (uint8_t)sa;
+        ep.qs[row / 16 + N / 32 + n / 32] = (uint8_t)sb;
+      }
+      store4(ep.C + row + n, silu_mul(a[0], b[0]), silu_mul(a[1], b[1]), silu_mul(a[2], b[2]),
+             silu_mul(a[3], b[3]));
+    } else if (MODE == kDgradQ) {   // 16 consecutive lanes hold 64 columns of the row
+      const int m = t.m0 + r;
+      const size_t row = (size_t)m * N;
+      const bool tok = r < t.vrows;
+      const float w = !tok ? 0.0f : ep.rw ? ep.rw[m] : 1.0f;
+      float va[4] = {0, 0, 0, 0}, vb[4] = {0, 0, 0, 0}, da[4], db[4], hw[4], dot = 0.0f;
+      if (tok) {
+        mx8_values4(*reinterpret_cast<const uint32_t*>(ep.q + 2 * row + n),
+                    ep.qs[row / 16 + n / 32], va);
+        mx8_values4(*reinterpret_cast<const uint32_t*>(ep.q + 2 * row + N + n),
+                    ep.qs[row / 16 + N / 32 + n / 32], vb);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const DgradQ d = dgradq(a[i], va[i], vb[i], w);
+        da[i] = d.da;
+        db[i] = d.db;
+        hw[i] = d.hw;
+        dot += d.dot;
+      }
+      store4(ep.C + 2 * row + n, da[0], da[1], da[2], da[3]);
+      store4(ep.C + 2 * row + N + n, db[0], db[1], db[2], db[3]);
+      store4(ep.dh + row + n, hw[0], hw[1], hw[2], hw[3]);
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) dot += __shfl_xor(dot, d);
+      if (ep.dots && (n & 63) == 0) ep.dots[(size_t)(n >> 6) * ep.m_cap + m] = dot;
+    } else if (MODE == kDgrad && r >= t.vrows) {   // pad row: zeros, its [a | b] is never read
       const float z[4] = {0.f, 0.f, 0.f, 0.f};
       dgrad4(ep, (size_t)(t.m0 + r) * N, n, z, uint2{0u, 0u}, uint2{0u, 0u});
     } else {
@@ -1576,7 +2079,7 @@ __global__ __launch_bounds__(256) void gg_f32_kernel(const float* __restrict__ A
                                                      const float* __restrict__ W1,
                                                      const float* __restrict__ W3, int ksplit,
                                                      Epi32 ep) {
-  constexpr bool FC1 = MODE == kFc1;
+  constexpr bool FC1 = is_fc1(MODE);
   const int N = ep.N;
   __shared__ float As[FM][FK + 1];
   __shared__ float B1[FN][FK + 1];
@@ -1714,6 +2217,13 @@ __global__ __launch_bounds__(256) void wg_f32_kernel(const float* __restrict__ P
 
 size_t grouped_workspace_bytes() { return (size_t)cu_count() * BM * BP * sizeof(float); }
 
+// The ring while an expert's row blocks fit about one column sweep (then every weight
+// panel comes from HBM once and the deeper lookahead pays); with more, later sweeps
+// find their panels in the caches and the ring only costs.
+static bool use_ring(int E, int64_t m_cap) {
+  return E <= RING_MAXE && m_cap <= (int64_t)(GROUP_M + 1) * BM * E;
+}
+
 // One m-grouped GEMM per segment with the MODE epilogue: C = A W^T, W [E][N][K]
 // (p_mn false), or C = A W with W [E][K][N] split at ksplit between W1 and W3 (p_mn
 // true). K: reduction width, ep.N: output columns.
@@ -1754,10 +2264,7 @@ static hipError_t launch_mgrouped(int dt, int mode, bool p_mn, const void* A, Se
   const bf16_t* w1 = static_cast<const bf16_t*>(W1);
   const bf16_t* w3 = static_cast<const bf16_t*>(W3);
   const int mc = (int)m_cap;
-  // the ring while an expert's row blocks fit about one column sweep (then every weight
-  // panel comes from HBM once and the deeper lookahead pays); with more, later sweeps
-  // find their panels in the caches and the ring only costs
-  const bool ring = E <= RING_MAXE && m_cap <= (int64_t)(GROUP_M + 1) * BM * E;
+  const bool ring = use_ring(E, m_cap);
   if (mode == kFc1) {
     if (ring)
       hipLaunchKernelGGL(gg_ring_kernel<kFc1>, grid, block, 0, s, a, sg, E, K, N, mc, w1, w3,
@@ -1836,6 +2343,116 @@ hipError_t launch_grouped_fc1_mx(const void* xq_perm, const void* xs_perm,
   if (slots)
     hipLaunchKernelGGL(gg_tail_reduce<kFc1>, dim3(4 * G), dim3(256), 0, s, sg, E, D / 2,
                        (int)m_cap, G, slots, ws, ep);
+  return hipGetLastError();
+}
+
+// Each row's weight: its slot's top-k weight, 0 for rows without a slot.
+__global__ __launch_bounds__(256) void row_weight_kernel(const int32_t* __restrict__ src_row,
+                                                         const float* __restrict__ topk_w,
+                                                         int nslots, int m_cap,
+                                                         float* __restrict__ rw) {
+  const int r = blockIdx.x * 256 + threadIdx.x;
+  if (r >= m_cap) return;
+  const int s = src_row[r];
+  rw[r] = s >= 0 && s < nslots ? topk_w[s] : 0.0f;
+}
+
+// Each slot's sum of its row's partial sums, in column order; 0 for slots without a row.
+__global__ __launch_bounds__(256) void row_dot_kernel(const int32_t* __restrict__ dst_row,
+                                                      const float* __restrict__ dots, int nslots,
+                                                      int m_cap, int parts,
+                                                      float* __restrict__ out) {
+  const int s = blockIdx.x * 256 + threadIdx.x;
+  if (s >= nslots) return;
+  const int r = dst_row[s];
+  float sum = 0.0f;
+  if (r >= 0 && r < m_cap)
+    for (int p = 0; p < parts; ++p) sum += dots[(size_t)p * m_cap + r];
+  out[s] = sum;
+}
+
+size_t ckpt8_scratch_bytes(int F, int64_t m_cap) {
+  return (size_t)m_cap * (1 + F / 64) * sizeof(float);
+}
+
+hipError_t launch_grouped_fc1_ckpt8(const void* x_perm, const int32_t* offsets,
+                                    const int32_t* counts, int E, int D, int F, int64_t m_cap,
+                                    const void* w1, const void* w3, void* h, void* q, void* qs,
+                                    void* workspace, size_t ws_bytes, hipStream_t s) {
+  const int G = cu_count(), mc = (int)m_cap;
+  float* ws = static_cast<float*>(workspace);
+  const int slots = ws ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20) : 0;
+  const Segs sg{offsets, counts, 0};
+  const Epi ep{static_cast<bf16_t*>(h), nullptr, nullptr, F, static_cast<uint8_t*>(q),
+               static_cast<uint8_t*>(qs), nullptr, nullptr, mc};
+  const bf16_t* a = static_cast<const bf16_t*>(x_perm);
+  const bf16_t *b1 = static_cast<const bf16_t*>(w1), *b3 = static_cast<const bf16_t*>(w3);
+  if (use_ring(E, m_cap))
+    hipLaunchKernelGGL(gg_ring_kernel<kFc1Q>, dim3(G), dim3(NTHR), 0, s, a, sg, E, D, F, mc, b1,
+                       b3, ep, ws, slots);
+  else
+    hipLaunchKernelGGL((gg_bf16_kernel<kFc1Q, false>), dim3(G), dim3(NTHR), 0, s, a, sg, E, D, F,
+                       mc, b1, b3, D, ep, ws, slots, MxScales{});
+  if (slots)
+    hipLaunchKernelGGL(gg_tail_reduce<kFc1Q>, dim3(4 * G), dim3(256), 0, s, sg, E, D, mc, G,
+                       slots, ws, ep);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offsets,
+                                      const int32_t* counts, int E, int D, int F, int64_t m_cap,
+                                      const void* w2, const void* q, const void* qs,
+                                      const int32_t* src_row, const int32_t* dst_row,
+                                      const float* topk_w, int nslots, void* dab, void* hw,
+                                      float* dtopk_w, void* scratch, void* workspace,
+                                      size_t ws_bytes, hipStream_t s) {
+  const int G = cu_count(), mc = (int)m_cap;
+  float* ws = static_cast<float*>(workspace);
+  const int slots = ws ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20) : 0;
+  const Segs sg{offsets, counts, 0};
+  float* rw = topk_w ? static_cast<float*>(scratch) : nullptr;
+  float* dots = dtopk_w ? static_cast<float*>(scratch) + m_cap : nullptr;
+  if (rw)
+    hipLaunchKernelGGL(row_weight_kernel, dim3((mc + 255) / 256), dim3(256), 0, s, src_row, topk_w,
+                       nslots, mc, rw);
+  const Epi ep{static_cast<bf16_t*>(dab), nullptr, static_cast<bf16_t*>(hw), F,
+               static_cast<uint8_t*>(const_cast<void*>(q)),
+               static_cast<uint8_t*>(const_cast<void*>(qs)), rw, dots, mc};
+  const bf16_t* w = static_cast<const bf16_t*>(w2);
+  hipLaunchKernelGGL((gg_bf16_kernel<kDgradQ, true>), dim3(G), dim3(NTHR), 0, s,
+                     static_cast<const bf16_t*>(dout_perm), sg, E, D, F, mc, w, w, D, ep, ws,
+                     slots, MxScales{});
+  if (slots)
+    hipLaunchKernelGGL(gg_tail_reduce<kDgradQ>, dim3(4 * G), dim3(256), 0, s, sg, E, D, mc, G,
+                       slots, ws, ep);
+  if (dtopk_w)
+    hipLaunchKernelGGL(row_dot_kernel, dim3((nslots + 255) / 256), dim3(256), 0, s, dst_row, dots,
+                       nslots, mc, F / 64, dtopk_w);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_mx4(bool fc1, const void* aq, const void* as, const int32_t* offsets,
+                              const int32_t* counts, int E, int K, int N, int64_t m_cap,
+                              const void* w1q, const void* w1s, const void* w3q, const void* w3s,
+                              void* out, void* workspace, size_t ws_bytes, hipStream_t s) {
+  const int G = cu_count();
+  float* ws = static_cast<float*>(workspace);
+  const int slots = ws ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20) : 0;
+  const Segs sg{offsets, counts, 0};
+  const Epi ep{static_cast<bf16_t*>(out), nullptr, nullptr, N};
+  const MxScales ms{static_cast<const uint32_t*>(as), static_cast<const uint32_t*>(w1s),
+                    static_cast<const uint32_t*>(w3s), m_cap};
+  const auto kern = fc1 ? gg_mx4_kernel<kFc1> : gg_mx4_kernel<kFc2>;
+  hipLaunchKernelGGL(kern, dim3(G), dim3(NTHR), 0, s, static_cast<const bf16_t*>(aq), sg, E,
+                     K / 2, N, (int)m_cap, static_cast<const bf16_t*>(w1q),
+                     static_cast<const bf16_t*>(w3q), ep, ws, slots, ms);
+  // the reduction counts k-steps as K / 64 bf16 values: here a step is 256 values
+  const int kred = (K + 255) / 256 * 64;
+  if (slots) {
+    const auto red = fc1 ? gg_tail_reduce<kFc1> : gg_tail_reduce<kFc2>;
+    hipLaunchKernelGGL(red, dim3(4 * G), dim3(256), 0, s, sg, E, kred, (int)m_cap, G, slots, ws,
+                       ep);
+  }
   return hipGetLastError();
 }
 

@@ -84,13 +84,51 @@ hipError_t launch_round_bf16(const float* x, uint16_t* y, int64_t n, hipStream_t
 hipError_t launch_quantize_mx(int dt, const void* x, int64_t R, int C, void* q, void* scales,
                               bool ksteps, hipStream_t s);
 
-// permute of the FP8 payload: the metadata of launch_permute, then the rows of the codes
-// (D bytes) and the scales (rows of D/32 bytes in, [D/128][m_cap] k-step words out)
-hipError_t launch_permute_mx(const void* xq, const void* xs, const int32_t* topk_idx, int T, int D,
-                             int E, int k, int m_tile, int64_t m_cap, void* xq_perm,
+// permute of the FP8 (bits 8) or FP4 (bits 4) payload: the metadata of launch_permute, then
+// the rows of the codes (D*bits/8 bytes) and the scales (rows of D/32 bytes in,
+// [D/128][m_cap] k-step words out)
+hipError_t launch_permute_mx(int bits, const void* xq, const void* xs, const int32_t* topk_idx,
+                             int T, int D, int E, int k, int m_tile, int64_t m_cap, void* xq_perm,
                              void* xs_perm, int32_t* counts, int32_t* offsets, int32_t* dst_row,
                              int32_t* src_row, int32_t* tile_expert, void* workspace,
                              int32_t* dev_err, hipStream_t s);
+
+// one MXFP4 product per segment (rows aq [m_cap, K/2] codes, scale words as [K/128][m_cap]):
+// fc1: out = silu(a)*b [m_cap, N] with w1, w3 [E, N, K/2]; else out = rows w1^T
+hipError_t launch_grouped_mx4(bool fc1, const void* aq, const void* as, const int32_t* offsets,
+                              const int32_t* counts, int E, int K, int N, int64_t m_cap,
+                              const void* w1q, const void* w1s, const void* w3q, const void* w3s,
+                              void* out, void* workspace, size_t ws_bytes, hipStream_t s);
+
+// MXFP4 rows: x [R, C] (dt) -> packed codes [R, C/2] and E8M0 scales, [R, C/32] bytes or
+// (ksteps) [C/128][R] words; and the values of MXFP4 (fp4) or MXFP8 rows in dt
+hipError_t launch_quantize_mx4(int dt, const void* x, int64_t R, int C, void* q, void* scales,
+                               bool ksteps, hipStream_t s);
+hipError_t launch_dequantize_mx(int dt, bool fp4, const void* q, const void* scales, int64_t R,
+                                int C, bool ksteps, void* out, hipStream_t s);
+
+// the masked grouped SwiGLU (bf16 rows, any cap) with MXFP4 weights w1, w3 [E, F, D/2],
+// w2 [E, D, F/2] and their scales in k-step words
+hipError_t launch_decode_mx4(const void* x, const int32_t* counts, int E, int D, int F, int cap,
+                             const void* w1q, const void* w1s, const void* w3q, const void* w3s,
+                             const void* w2q, const void* w2s, void* h, void* y, hipStream_t s);
+
+// bf16 fc1 that keeps [a | b] as e4m3 codes q [m_cap, 2F] and scale bytes qs [m_cap, 2F/32]
+hipError_t launch_grouped_fc1_ckpt8(const void* x_perm, const int32_t* offsets,
+                                    const int32_t* counts, int E, int D, int F, int64_t m_cap,
+                                    const void* w1, const void* w3, void* h, void* q, void* qs,
+                                    void* workspace, size_t ws_bytes, hipStream_t s);
+
+// its use in the backward: u = dout_perm w2[e] (unweighted rows), dab, hw = weighted h and,
+// when set, dtopk_w [nslots]; scratch (ckpt8_scratch_bytes) when topk_w is set
+size_t ckpt8_scratch_bytes(int F, int64_t m_cap);
+hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offsets,
+                                      const int32_t* counts, int E, int D, int F, int64_t m_cap,
+                                      const void* w2, const void* q, const void* qs,
+                                      const int32_t* src_row, const int32_t* dst_row,
+                                      const float* topk_w, int nslots, void* dab, void* hw,
+                                      float* dtopk_w, void* scratch, void* workspace,
+                                      size_t ws_bytes, hipStream_t s);
 
 // dh = dy_perm w2[e] (w2 [E,D,F]), then [da | db] from ab -> dab; dh stored if non-null
 hipError_t launch_grouped_dgrad_swiglu(int dt, const void* dy_perm, const int32_t* offsets,

@@ -5,7 +5,7 @@
 #include <mutex>
 
 #include "moe.h"
-#include "kernels.hpp"
+#include "checks.hpp"
 
 namespace moe {
 
@@ -26,24 +26,7 @@ int cu_count() {
 
 }  // namespace moe
 
-namespace {
-
-constexpr int kMaxExperts = 1024;
-constexpr int kMaxK = moe::kMaxTopK;
-constexpr int kMaxDim = 1 << 16;
-
-bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool dim_ok(int d) { return d >= 64 && d <= kMaxDim && d % 64 == 0; }
-bool mtile_ok(int mt) { return mt == 16 || mt == 32 || mt == 64 || mt == 128 || mt == 256; }
-bool dtype_ok(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
-bool tk_ok(int T, int k) { return T >= 1 && (int64_t)T * k <= (1 << 30); }
-// masked slabs: a multiple of 16 rows each, E*cap rows addressable with int32
-bool cap_ok(int E, int cap) { return cap >= 16 && cap % 16 == 0 && (int64_t)E * cap <= INT32_MAX; }
-
-moe_status_t hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
-
-}  // namespace
+using namespace moe;
 
 extern "C" {
 
@@ -250,7 +233,7 @@ moe_status_t moe_permute_mxfp8(const void* xq, const void* xs, const int32_t* to
   const int64_t need = moe_capacity(T, k, E, m_tile);
   if (m_cap < need || m_cap % m_tile != 0 || m_cap > INT32_MAX) return MOE_ECAPACITY;
   if (ws_bytes < moe::permute_workspace_bytes(T, k, E)) return MOE_EWORKSPACE;
-  return hip_status(moe::launch_permute_mx(xq, xs, topk_idx, T, D, E, k, m_tile, m_cap, xq_perm,
+  return hip_status(moe::launch_permute_mx(8, xq, xs, topk_idx, T, D, E, k, m_tile, m_cap, xq_perm,
                                            xs_perm, counts, offsets, dst_row, src_row,
                                            tile_expert, workspace, dev_err,
                                            static_cast<hipStream_t>(stream)));

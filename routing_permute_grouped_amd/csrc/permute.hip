@@ -923,8 +923,8 @@ hipError_t launch_permute_masked(int dt, const void* x, const int32_t* topk_idx,
   return launch_copy(dt, x, T, D, k, 0, dst_row, counts, nullptr, x_masked, s);
 }
 
-hipError_t launch_permute_mx(const void* xq, const void* xs, const int32_t* topk_idx, int T, int D,
-                             int E, int k, int m_tile, int64_t m_cap, void* xq_perm,
+hipError_t launch_permute_mx(int bits, const void* xq, const void* xs, const int32_t* topk_idx,
+                             int T, int D, int E, int k, int m_tile, int64_t m_cap, void* xq_perm,
                              void* xs_perm, int32_t* counts, int32_t* offsets, int32_t* dst_row,
                              int32_t* src_row, int32_t* tile_expert, void* workspace,
                              int32_t* dev_err, hipStream_t s) {
@@ -936,10 +936,10 @@ hipError_t launch_permute_mx(const void* xq, const void* xs, const int32_t* topk
   hipLaunchKernelGGL(rank_kernel<false>, dim3(nbh + 1), dim3(kThreads), 0, s, topk_idx, T, k, E,
                      m_tile, 0, m_cap, nbh, scanned, hist, bad, counts, offsets, tile_expert, dev_err,
                      dst_row, src_row);
-  // the code rows are copied as raw bytes (D bytes = D/2 two-byte units, whole 16-byte
+  // the code rows are copied as raw bytes (D*bits/8 bytes in two-byte units, whole 16-byte
   // chunks as D % 128 == 0); pad rows get zero bytes (code 0 is +0). The scales go into
   // k-step words, zero for pad rows.
-  const hipError_t e = launch_copy(kBF16, xq, T, D / 2, k, E, dst_row, counts, offsets, xq_perm, s);
+  const hipError_t e = launch_copy(kBF16, xq, T, D * bits / 16, k, E, dst_row, counts, offsets, xq_perm, s);
   if (e != hipSuccess) return e;
   const int nsw = D / 128;
   const int grid = (int)std::min<int64_t>(8 * cu_count(),

@@ -7,11 +7,12 @@ experts as one expert over all tokens)] -> combine, following the layer order of
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 
 from . import _binding as B
+from . import _binding_mx as X
 
 
 @dataclass
@@ -45,14 +46,22 @@ def moe_layer(x: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, w2: torch.Ten
               m_tile: int, wg: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
               topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
               shared: Optional[SharedExperts] = None, renorm: bool = False,
-              check: bool = False, split_k: bool = True, save_for_backward: bool = False) -> dict:
+              check: bool = False, split_k: bool = True,
+              save_for_backward: Union[bool, str] = False) -> dict:
     """Run the layer; returns every intermediate (dict). With routing given
     (``topk_idx``/``topk_w``) the route step is skipped. ``check`` synchronises and
     raises if the permute saw an expert index outside [-1, E). ``split_k`` gives the
     grouped GEMMs a workspace so they can split a partly filled last round of tiles.
     ``save_for_backward`` also keeps fc1's pre-activations (``ab``, and ``shared_ab`` /
-    ``shared_h`` for the shared experts), which ``moe_layer_backward`` reads."""
+    ``shared_h`` for the shared experts), which ``moe_layer_backward`` reads;
+    ``save_for_backward="mxfp8"`` (bf16) keeps them in 8 bits instead (``ab_codes``,
+    ``ab_scales``, and ``shared_`` ones), and returns neither ``x_perm``, ``h`` nor ``y_perm``
+    (nor ``shared_h``), which that backward does without: per routed row 2F*33/32 bytes in
+    place of 4D + 6F."""
     E, F, D = w1.shape
+    ckpt8 = save_for_backward == "mxfp8"
+    if isinstance(save_for_backward, str) and not ckpt8:
+        raise ValueError(f"save_for_backward: {save_for_backward!r}, expected True, False or 'mxfp8'")
     res = {}
     if topk_idx is None:
         topk_idx, topk_w, _ = B.moe_route(x, wg, k, bias=bias, renorm=renorm)
@@ -61,7 +70,15 @@ def moe_layer(x: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, w2: torch.Ten
     res.update(p)
     m_cap = p["m_cap"]
     ws = B.grouped_workspace(x.device) if split_k else None
-    if save_for_backward:
+    if ckpt8:
+        h, res["ab_codes"], res["ab_scales"] = X.moe_grouped_fc1_swiglu_ckpt8(
+            p["x_perm"], p["offsets"], p["tile_expert"], w1, w3, m_tile, m_cap, workspace=ws,
+            counts=p["counts"])
+        y = torch.empty((m_cap, D), dtype=x.dtype, device=x.device)
+        B.moe_grouped_fc2(h, p["offsets"], p["tile_expert"], w2, m_tile, m_cap, y, workspace=ws,
+                          counts=p["counts"])
+        del res["x_perm"]
+    elif save_for_backward:
         h = torch.empty((m_cap, F), dtype=x.dtype, device=x.device)
         ab = torch.empty((m_cap, 2 * F), dtype=x.dtype, device=x.device)
         y = torch.empty((m_cap, D), dtype=x.dtype, device=x.device)
@@ -73,11 +90,19 @@ def moe_layer(x: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, w2: torch.Ten
     else:
         h, y = B.moe_grouped_swiglu(p["x_perm"], p["offsets"], p["tile_expert"], w1, w3, w2,
                                     m_tile, m_cap=m_cap, workspace=ws, counts=p["counts"])
-    res["h"], res["y_perm"] = h, y
+    if not ckpt8:
+        res["h"], res["y_perm"] = h, y
     sh = None
     if shared is not None:
         rows = DenseRows(x.shape[0], m_tile, x.device)
-        if save_for_backward:
+        if ckpt8:
+            hs, res["shared_ab_codes"], res["shared_ab_scales"] = X.moe_grouped_fc1_swiglu_ckpt8(
+                x, rows.offsets, rows.tile_expert, shared.w1, shared.w3, m_tile, rows.m_cap,
+                workspace=ws, rows_used=rows.T)
+            ys = torch.empty((rows.m_cap, D), dtype=x.dtype, device=x.device)
+            B.moe_grouped_fc2(hs, rows.offsets, rows.tile_expert, shared.w2, m_tile, rows.m_cap,
+                              ys, workspace=ws)
+        elif save_for_backward:
             SF = shared.w1.shape[1]
             hs = torch.empty((rows.m_cap, SF), dtype=x.dtype, device=x.device)
             abs_ = torch.empty((rows.m_cap, 2 * SF), dtype=x.dtype, device=x.device)
@@ -189,6 +214,98 @@ def moe_layer_mxfp8(x: torch.Tensor, mw: MxWeights, w2: torch.Tensor, k: int, m_
     return res
 
 
+@dataclass
+class Mx4Weights:
+    """The experts' weights quantized once to MXFP4: codes (two a byte) w1q, w3q [E,F,D/2],
+    w2q [E,D,F/2], and their E8M0 scales in the products' k-step words (w1s, w3s uint8
+    [D/128, E*F, 4], w2s [F/128, E*D, 4])."""
+    w1q: torch.Tensor
+    w1s: torch.Tensor
+    w3q: torch.Tensor
+    w3s: torch.Tensor
+    w2q: torch.Tensor
+    w2s: torch.Tensor
+
+    @staticmethod
+    def quantize(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor) -> "Mx4Weights":
+        w1q, w1s = X.moe_quantize_mxfp4(w1, layout=B.MOE_MX_KSTEPS)
+        w3q, w3s = X.moe_quantize_mxfp4(w3, layout=B.MOE_MX_KSTEPS)
+        w2q, w2s = X.moe_quantize_mxfp4(w2, layout=B.MOE_MX_KSTEPS)
+        return Mx4Weights(w1q, w1s, w3q, w3s, w2q, w2s)
+
+
+def moe_layer_mxfp4(x: torch.Tensor, mw: Mx4Weights, k: int, m_tile: int,
+                    wg: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                    topk_idx: Optional[torch.Tensor] = None,
+                    topk_w: Optional[torch.Tensor] = None,
+                    shared: Optional[SharedExperts] = None, renorm: bool = False,
+                    split_k: bool = True) -> dict:
+    """The layer (bf16 x) with 4-bit weights and 4-bit rows in both products: route on the bf16
+    x -> quantize x -> permute codes and scales -> fc1 and fc2 on the scaled FP4 MFMA, h
+    quantized between them [-> shared experts, bf16] -> combine."""
+    E = mw.w1q.shape[0]
+    res = {}
+    if topk_idx is None:
+        topk_idx, topk_w, _ = B.moe_route(x, wg, k, bias=bias, renorm=renorm)
+    res["topk_idx"], res["topk_w"] = topk_idx, topk_w
+    B._dtype(x, "x", torch.bfloat16)
+    xq, xs = X.moe_quantize_mxfp4(x)
+    res["xq"], res["xs"] = xq, xs
+    p = X.moe_permute_mxfp4(xq, xs, topk_idx, E, m_tile)
+    res.update(p)
+    m_cap = p["m_cap"]
+    ws = B.grouped_workspace(x.device) if split_k else None
+    h = X.moe_grouped_fc1_swiglu_mxfp4(p["xq_perm"], p["xs_perm"], p["offsets"],
+                                       p["tile_expert"], mw.w1q, mw.w1s, mw.w3q, mw.w3s, m_tile,
+                                       m_cap, workspace=ws, counts=p["counts"])
+    hq, hs = X.moe_quantize_mxfp4(h, layout=B.MOE_MX_KSTEPS)
+    y = X.moe_grouped_fc2_mxfp4(hq, hs, p["offsets"], p["tile_expert"], mw.w2q, mw.w2s, m_tile,
+                                m_cap, workspace=ws, counts=p["counts"])
+    res["h"], res["y_perm"] = h, y
+    sh = None
+    if shared is not None:
+        rows = DenseRows(x.shape[0], m_tile, x.device)
+        _, ys = B.moe_grouped_swiglu(x, rows.offsets, rows.tile_expert, shared.w1, shared.w3,
+                                     shared.w2, m_tile, m_cap=rows.m_cap, workspace=ws,
+                                     rows_used=rows.T)
+        sh = ys[: x.shape[0]]
+        res["shared"] = sh
+    res["out"] = B.moe_combine(y, p["dst_row"], topk_w, shared=sh, m_cap=m_cap)
+    return res
+
+
+def moe_layer_masked_mxfp4(x: torch.Tensor, mw: Mx4Weights, k: int, cap: int,
+                           wg: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None,
+                           topk_idx: Optional[torch.Tensor] = None,
+                           topk_w: Optional[torch.Tensor] = None,
+                           shared: Optional[SharedExperts] = None, renorm: bool = False,
+                           split_k: bool = True, shared_m_tile: int = 128) -> dict:
+    """moe_layer_masked (bf16 x) with 4-bit expert weights: the rows stay bf16, the weights are
+    streamed in 4 bits. ``split_k`` and ``shared_m_tile`` concern the shared experts."""
+    E = mw.w1q.shape[0]
+    res = {}
+    if topk_idx is None:
+        topk_idx, topk_w, _ = B.moe_route(x, wg, k, bias=bias, renorm=renorm)
+    res["topk_idx"], res["topk_w"] = topk_idx, topk_w
+    p = B.moe_permute_masked(x, topk_idx, E, cap)
+    res.update(p)
+    h, y = X.moe_grouped_swiglu_masked_mxfp4(p["x_masked"], p["counts"], mw.w1q, mw.w1s, mw.w3q,
+                                             mw.w3s, mw.w2q, mw.w2s, cap)
+    res["h"], res["y_perm"] = h, y
+    sh = None
+    if shared is not None:
+        ws = B.grouped_workspace(x.device) if split_k else None
+        rows = DenseRows(x.shape[0], shared_m_tile, x.device)
+        _, ys = B.moe_grouped_swiglu(x, rows.offsets, rows.tile_expert, shared.w1, shared.w3,
+                                     shared.w2, shared_m_tile, m_cap=rows.m_cap, workspace=ws,
+                                     rows_used=rows.T)
+        sh = ys[: x.shape[0]]
+        res["shared"] = sh
+    res["out"] = B.moe_combine(y, p["dst_row"], topk_w, shared=sh, m_cap=p["m_cap"])
+    return res
+
+
 def _experts_backward(dy, x_rows, ab, h, offsets, tile_expert, w1, w3, w2, m_tile, m_cap, ws,
                       rows_used=None, counts=None):
     """dgrad and wgrad of one grouped SwiGLU FFN over rows [0, m_cap) (section 5 of
@@ -206,6 +323,52 @@ def _experts_backward(dy, x_rows, ab, h, offsets, tile_expert, w1, w3, w2, m_til
     return dab, dX, dw1, dw3, dw2
 
 
+def _experts_backward_ckpt8(dout_rows, x_rows, codes, scales, offsets, tile_expert, w1, w3, w2,
+                            m_tile, m_cap, ws, rows_used=None, counts=None, **weights):
+    """_experts_backward from an 8-bit checkpoint, for the unweighted output gradient's rows;
+    ``weights``: topk_w with src_row and dst_row. ``x_rows`` is called for the rows of x once
+    they are needed. Returns (dab, dX, dw1, dw3, dw2, dtopk_w)."""
+    F, D = w1.shape[1], w1.shape[2]
+    ru, c = rows_used, counts
+    dab, hw, dtw = X.moe_grouped_dgrad_swiglu_ckpt8(dout_rows, offsets, tile_expert, w2, codes,
+                                                    scales, m_tile, m_cap, workspace=ws,
+                                                    rows_used=ru, counts=c, **weights)
+    dw2, _ = B.moe_grouped_wgrad(dout_rows, hw, offsets, m_tile, m_cap, NS=D, rows_used=ru,
+                                 counts=c)
+    del hw
+    dX = B.moe_grouped_dgrad_fc1(dab, offsets, tile_expert, w1, w3, m_tile, m_cap, workspace=ws,
+                                 rows_used=ru, counts=c)
+    dw1, dw3 = B.moe_grouped_wgrad(dab, x_rows(), offsets, m_tile, m_cap, NS=F, rows_used=ru,
+                                   counts=c)
+    return dab, dX, dw1, dw3, dw2, dtw
+
+
+def _layer_backward_ckpt8(fwd, dout, x, w1, w3, w2, m_tile, shared, split_k):
+    """moe_layer_backward from ``moe_layer(save_for_backward="mxfp8")``: the output gradient
+    and x are moved to the permuted rows by the forward's routing, the top-k weights are
+    applied behind the dgrad of fc2."""
+    E = w1.shape[0]
+    m_cap, offs, te, counts = fwd["m_cap"], fwd["offsets"], fwd["tile_expert"], fwd["counts"]
+    ws = B.grouped_workspace(x.device) if split_k else None
+    rows = lambda t: B.moe_permute(t, fwd["topk_idx"], E, m_tile, m_cap)["x_perm"]  # noqa: E731
+    res = {}
+    res["dab"], dX, res["dw1"], res["dw3"], res["dw2"], res["dtopk_w"] = _experts_backward_ckpt8(
+        rows(dout), lambda: rows(x), fwd["ab_codes"], fwd["ab_scales"], offs, te, w1, w3, w2,
+        m_tile, m_cap, ws, counts=counts, src_row=fwd["src_row"], dst_row=fwd["dst_row"],
+        topk_w=fwd["topk_w"])
+    res["dx_perm"] = dX
+    dxs = None
+    if shared is not None:
+        T = x.shape[0]
+        sr = DenseRows(T, m_tile, x.device)
+        _, dXs, res["dws1"], res["dws3"], res["dws2"], _ = _experts_backward_ckpt8(
+            dout, lambda: x, fwd["shared_ab_codes"], fwd["shared_ab_scales"], sr.offsets,
+            sr.tile_expert, shared.w1, shared.w3, shared.w2, m_tile, sr.m_cap, ws, rows_used=T)
+        dxs = res["dx_shared"] = dXs[:T]
+    res["dx"] = B.moe_combine(dX, fwd["dst_row"], None, shared=dxs, m_cap=m_cap)
+    return res
+
+
 def moe_layer_backward(fwd: dict, dout: torch.Tensor, x: torch.Tensor, w1: torch.Tensor,
                        w3: torch.Tensor, w2: torch.Tensor, m_tile: int,
                        shared: Optional[SharedExperts] = None, split_k: bool = True) -> dict:
@@ -215,7 +378,10 @@ def moe_layer_backward(fwd: dict, dout: torch.Tensor, x: torch.Tensor, w1: torch
     wgrad, permute -> unpermute (moe_combine without weights). Routing is taken as
     given; its weights get their gradient ``dtopk_w``. Weight gradients are float32
     (``dw1``, ``dw3`` [E,F,D], ``dw2`` [E,D,F]; for the shared experts ``dws1``, ``dws3``
-    [1,S*Fs,D] and ``dws2`` [1,D,S*Fs], the concatenated layout of SharedExperts)."""
+    [1,S*Fs,D] and ``dws2`` [1,D,S*Fs], the concatenated layout of SharedExperts). After
+    ``save_for_backward="mxfp8"`` the same from the 8-bit checkpoint, without ``dy_perm``."""
+    if "ab_codes" in fwd:
+        return _layer_backward_ckpt8(fwd, dout, x, w1, w3, w2, m_tile, shared, split_k)
     m_cap = fwd["m_cap"]
     offs, te = fwd["offsets"], fwd["tile_expert"]
     ws = B.grouped_workspace(x.device) if split_k else None
