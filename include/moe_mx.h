@@ -116,7 +116,8 @@ moe_status_t moe_grouped_swiglu_masked_mxfp4(const void* x_masked, const int32_t
 /*
  * moe_grouped_fc1_swiglu_ckpt8 - moe_grouped_fc1_swiglu (bf16) that keeps the
  * pre-activations for the backward as MXFP8 in place of bf16:
- *   -> h [m_cap,F] bf16 (the same values as moe_grouped_fc1_swiglu)
+ *   -> h [m_cap,F] bf16, bit for bit moe_grouped_fc1_swiglu's without a workspace (with one
+ *                    the two calls may cut different tiles over k: another order of sums)
  *      ab_codes [m_cap,2F] e4m3 codes of [a | b], ab_scales [m_cap,2F/32] bytes
  * Blocks are 32 consecutive columns of a or of b, quantised from the float32 sums. Pad rows
  * give exact zeros. Per row 2F*33/32 bytes in place of 4F. Arguments otherwise, workspace
@@ -144,9 +145,9 @@ moe_status_t moe_grouped_fc1_swiglu_ckpt8(const void* x_perm, const int32_t* off
  * each rounded once to its type. The sums over F run in a fixed order. Pad rows give exact
  * zeros; rows at or past offsets[E] are neither read nor written.
  * src_row [m_cap], dst_row [T,k] as moe_permute writes them; T and k give topk_w's and
- * dtopk_w's size. topk_w needs src_row and `scratch`, dtopk_w needs topk_w and dst_row;
- * without topk_w all of these may be NULL (T and k are then not looked at). scratch: device
- * memory of at least moe_ckpt8_scratch_bytes(F, m_cap), 16-byte aligned, clobbered; calls
+ * dtopk_w's size. topk_w needs src_row; dtopk_w needs topk_w, dst_row and `scratch`; without
+ * topk_w all of these may be NULL (T and k are then not looked at). scratch: device memory
+ * of at least moe_ckpt8_scratch_bytes(F, m_cap), 16-byte aligned, clobbered; calls
  * that share it or the workspace must not overlap.
  * Sizes, m_tile and workspace as moe_grouped_swiglu.
  * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_ECAPACITY, MOE_EWORKSPACE (scratch), MOE_EHIP.
@@ -161,7 +162,7 @@ moe_status_t moe_grouped_dgrad_swiglu_ckpt8(const void* dout_perm, const int32_t
                                             void* scratch, size_t scratch_bytes,
                                             void* workspace, size_t ws_bytes, void* stream);
 
-/* Scratch bytes of moe_grouped_dgrad_swiglu_ckpt8 with topk_w. Returns 0 on bad sizes. */
+/* Scratch bytes of moe_grouped_dgrad_swiglu_ckpt8 with dtopk_w. Returns 0 on bad sizes. */
 size_t moe_ckpt8_scratch_bytes(int F, int64_t m_cap);
 
 #ifdef __cplusplus

@@ -35,22 +35,40 @@ for _name, _res, _args in MX_SIGNATURES:
     _fn.restype, _fn.argtypes = _res, _args
 
 
-def _run(name: str, stream, tensors: dict, args) -> None:
-    """Check that every tensor is contiguous and on the first one's GPU, and call ``name``
-    there; ``args`` maps the pointers by name and the stream to the C arguments."""
-    ptr, dev = {}, None
-    for n, t in tensors.items():
-        if t is not None:
-            if not t.is_cuda:
+# The current stream's handle of a device: what torch.cuda.current_stream(dev).cuda_stream
+# gives, without making the Stream object (1.1 us of a call that takes 8).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _run(name: str, stream, *args) -> None:
+    """Call ``name`` with its C arguments in order, the stream last. A tensor is given as
+    (argument name, tensor or None); every one must be contiguous and on the first one's GPU,
+    where the call is made."""
+    dev, c = None, []
+    for a in args:
+        if a.__class__ is not tuple:
+            c.append(a)
+            continue
+        n, t = a
+        if t is None:
+            c.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
                 raise ValueError(f"{n}: tensor must live on the GPU")
-            if not t.is_contiguous():
-                raise ValueError(f"{n}: tensor must be contiguous")
-            dev = t.device if dev is None else dev
-            if t.device != dev:
-                raise ValueError(f"{n}: on {t.device}, expected {dev}")
-        ptr[n] = None if t is None else t.data_ptr()
+            if dev is not None:
+                raise ValueError(f"{n}: on cuda:{d}, expected cuda:{dev}")
+            dev = d
+        if not t.is_contiguous():
+            raise ValueError(f"{n}: tensor must be contiguous")
+        c.append(t.data_ptr())
+    fn = getattr(B.lib, name)
+    if torch.cuda.current_device() == dev:
+        B._check(name, fn(*c, _raw_stream(dev) if stream is None else B._stream(stream)))
+        return
     with torch.cuda.device(dev):
-        B._check(name, getattr(B.lib, name)(*args(ptr, B._stream(stream))))
+        B._check(name, fn(*c, _raw_stream(dev) if stream is None else B._stream(stream)))
 
 
 def _scale_bytes(rows: int, C: int) -> int:
@@ -85,8 +103,8 @@ def moe_quantize_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     if scales is None:
         shape = (C // 128, R, 4) if layout == B.MOE_MX_KSTEPS else (*x.shape[:-1], C // 32)
         scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
-    _run("moe_quantize_mxfp4", stream, dict(x=x, q=q, scales=scales), lambda p, s: (
-        B._dt(x), p["x"], R, C, p["q"], p["scales"], layout, s))
+    _run("moe_quantize_mxfp4", stream, B._dt(x), ("x", x), R, C, ("q", q), ("scales", scales),
+         layout)
     return q, scales
 
 
@@ -99,8 +117,7 @@ def _dequantize(name: str, per: int, q, scales, out, layout, dtype, stream) -> t
         out = torch.empty((*q.shape[:-1], C), dtype=dtype, device=q.device)
     B._layer_dtype(out, "out")
     B._numel(out, "out", R * C)
-    _run(name, stream, dict(q=q, scales=scales, out=out), lambda p, s: (
-        B._dt(out), p["q"], p["scales"], R, C, layout, p["out"], s))
+    _run(name, stream, B._dt(out), ("q", q), ("scales", scales), R, C, layout, ("out", out))
     return out
 
 
@@ -151,14 +168,12 @@ def moe_permute_mxfp4(xq: torch.Tensor, xs: torch.Tensor, topk_idx: torch.Tensor
     o.setdefault("tile_expert", torch.empty(m_cap // m_tile, **i32))
     o.setdefault("dev_err", torch.empty(1, **i32))
     o.setdefault("workspace", torch.empty(ws, dtype=torch.uint8, device=dev))
-    names = ("xq_perm", "xs_perm", "counts", "offsets", "dst_row", "src_row", "tile_expert",
-             "dev_err", "workspace")
     wsb = o["workspace"].numel() * o["workspace"].element_size()
-    _run("moe_permute_mxfp4", stream,
-         dict(xq=xq, xs=xs, topk_idx=topk_idx, **{n: o[n] for n in names}), lambda p, s: (
-             p["xq"], p["xs"], p["topk_idx"], T, D, E, k, m_tile, m_cap, p["xq_perm"],
-             p["xs_perm"], p["counts"], p["offsets"], p["dst_row"], p["src_row"],
-             p["tile_expert"], p["workspace"], wsb, p["dev_err"], s))
+    _run("moe_permute_mxfp4", stream, ("xq", xq), ("xs", xs), ("topk_idx", topk_idx), T, D, E, k,
+         m_tile, m_cap, ("xq_perm", o["xq_perm"]), ("xs_perm", o["xs_perm"]),
+         ("counts", o["counts"]), ("offsets", o["offsets"]), ("dst_row", o["dst_row"]),
+         ("src_row", o["src_row"]), ("tile_expert", o["tile_expert"]),
+         ("workspace", o["workspace"]), wsb, ("dev_err", o["dev_err"]))
     o["m_cap"] = m_cap
     return o
 
@@ -204,13 +219,10 @@ def moe_grouped_fc1_swiglu_mxfp4(xq_perm: torch.Tensor, xs_perm: torch.Tensor,
     B._rows(h, "h", m_cap, F, torch.bfloat16)
     if h is None:
         h = torch.empty((m_cap, F), dtype=torch.bfloat16, device=xq_perm.device)
-    _run("moe_grouped_fc1_swiglu_mxfp4", stream,
-         dict(xq_perm=xq_perm, xs_perm=xs_perm, offsets=offsets, counts=counts,
-              tile_expert=tile_expert, w1q=w1q, w1s=w1s, w3q=w3q, w3s=w3s, h=h,
-              workspace=workspace), lambda p, s: (
-             p["xq_perm"], p["xs_perm"], p["offsets"], p["counts"], p["tile_expert"], E, D, F,
-             m_tile, m_cap, p["w1q"], p["w1s"], p["w3q"], p["w3s"], p["h"], p["workspace"],
-             _wsz(workspace), s))
+    _run("moe_grouped_fc1_swiglu_mxfp4", stream, ("xq_perm", xq_perm), ("xs_perm", xs_perm),
+         ("offsets", offsets), ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile,
+         m_cap, ("w1q", w1q), ("w1s", w1s), ("w3q", w3q), ("w3s", w3s), ("h", h),
+         ("workspace", workspace), _wsz(workspace))
     return h
 
 
@@ -231,11 +243,9 @@ def moe_grouped_fc2_mxfp4(hq: torch.Tensor, hs: torch.Tensor, offsets: torch.Ten
     B._rows(y_perm, "y_perm", m_cap, D, torch.bfloat16)
     if y_perm is None:
         y_perm = torch.empty((m_cap, D), dtype=torch.bfloat16, device=hq.device)
-    _run("moe_grouped_fc2_mxfp4", stream,
-         dict(hq=hq, hs=hs, offsets=offsets, counts=counts, tile_expert=tile_expert, w2q=w2q,
-              w2s=w2s, y_perm=y_perm, workspace=workspace), lambda p, s: (
-             p["hq"], p["hs"], p["offsets"], p["counts"], p["tile_expert"], E, D, F, m_tile,
-             m_cap, p["w2q"], p["w2s"], p["y_perm"], p["workspace"], _wsz(workspace), s))
+    _run("moe_grouped_fc2_mxfp4", stream, ("hq", hq), ("hs", hs), ("offsets", offsets),
+         ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w2q", w2q),
+         ("w2s", w2s), ("y_perm", y_perm), ("workspace", workspace), _wsz(workspace))
     return y_perm
 
 
@@ -259,11 +269,9 @@ def moe_grouped_swiglu_masked_mxfp4(x_masked: torch.Tensor, counts: torch.Tensor
         h = torch.empty((E * cap, F), dtype=torch.bfloat16, device=dev)
     if y is None:
         y = torch.empty((E * cap, D), dtype=torch.bfloat16, device=dev)
-    _run("moe_grouped_swiglu_masked_mxfp4", stream,
-         dict(x_masked=x_masked, counts=counts, w1q=w1q, w1s=w1s, w3q=w3q, w3s=w3s, w2q=w2q,
-              w2s=w2s, h=h, y=y), lambda p, s: (
-             p["x_masked"], p["counts"], E, D, F, cap, p["w1q"], p["w1s"], p["w3q"], p["w3s"],
-             p["w2q"], p["w2s"], p["h"], p["y"], s))
+    _run("moe_grouped_swiglu_masked_mxfp4", stream, ("x_masked", x_masked), ("counts", counts), E,
+         D, F, cap, ("w1q", w1q), ("w1s", w1s), ("w3q", w3q), ("w3s", w3s), ("w2q", w2q),
+         ("w2s", w2s), ("h", h), ("y", y))
     return h, y
 
 
@@ -297,13 +305,10 @@ def moe_grouped_fc1_swiglu_ckpt8(x_perm: torch.Tensor, offsets: torch.Tensor,
         ab_codes = torch.empty((m_cap, 2 * F), dtype=torch.uint8, device=dev)
     if ab_scales is None:
         ab_scales = torch.empty((m_cap, F // 16), dtype=torch.uint8, device=dev)
-    _run("moe_grouped_fc1_swiglu_ckpt8", stream,
-         dict(x_perm=x_perm, offsets=offsets, counts=counts, tile_expert=tile_expert, w1=w1,
-              w3=w3, h=h, ab_codes=ab_codes, ab_scales=ab_scales, workspace=workspace),
-         lambda p, s: (
-             p["x_perm"], p["offsets"], p["counts"], p["tile_expert"], E, D, F, m_tile, m_cap,
-             p["w1"], p["w3"], p["h"], p["ab_codes"], p["ab_scales"], p["workspace"],
-             _wsz(workspace), s))
+    _run("moe_grouped_fc1_swiglu_ckpt8", stream, ("x_perm", x_perm), ("offsets", offsets),
+         ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w1", w1),
+         ("w3", w3), ("h", h), ("ab_codes", ab_codes), ("ab_scales", ab_scales),
+         ("workspace", workspace), _wsz(workspace))
     return h, ab_codes, ab_scales
 
 
@@ -370,13 +375,10 @@ def moe_grouped_dgrad_swiglu_ckpt8(dout_perm: torch.Tensor, offsets: torch.Tenso
             dtopk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
         if scratch is None:
             scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-    _run("moe_grouped_dgrad_swiglu_ckpt8", stream,
-         dict(dout_perm=dout_perm, offsets=offsets, counts=counts, tile_expert=tile_expert,
-              w2=w2, ab_codes=ab_codes, ab_scales=ab_scales, src_row=src_row, dst_row=dst_row,
-              topk_w=topk_w, dab=dab, hw=hw, dtopk_w=dtopk_w, scratch=scratch,
-              workspace=workspace), lambda p, s: (
-             p["dout_perm"], p["offsets"], p["counts"], p["tile_expert"], E, D, F, m_tile, m_cap,
-             p["w2"], p["ab_codes"], p["ab_scales"], p["src_row"], p["dst_row"], p["topk_w"], T,
-             k, p["dab"], p["hw"], p["dtopk_w"], p["scratch"], _wsz(scratch), p["workspace"],
-             _wsz(workspace), s))
+    _run("moe_grouped_dgrad_swiglu_ckpt8", stream, ("dout_perm", dout_perm), ("offsets", offsets),
+         ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w2", w2),
+         ("ab_codes", ab_codes), ("ab_scales", ab_scales), ("src_row", src_row),
+         ("dst_row", dst_row), ("topk_w", topk_w), T, k, ("dab", dab), ("hw", hw),
+         ("dtopk_w", dtopk_w), ("scratch", scratch), _wsz(scratch), ("workspace", workspace),
+         _wsz(workspace))
     return dab, hw, dtopk_w

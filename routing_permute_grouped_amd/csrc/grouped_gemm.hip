@@ -91,7 +91,8 @@ __device__ __forceinline__ void store4(bf16_t* p, float a, float b, float c, flo
 //   kFc1Q  as kFc1, with [a | b] kept as e4m3 codes q [m][2N] and E8M0 scales
 //          qs [m][2N/32], quantised from the float32 sums
 //   kDgradQ  the sums are u = dout w2[e] of the unweighted output gradient; with (a, b)
-//          from such a checkpoint and the row's weight w (rw [m], null: 1):
+//          from such a checkpoint and the row's weight w (tw[src[m]], 0 without a slot;
+//          tw null: 1):
 //          [w*u*b*silu'(a) | w*u*silu(a)] -> C [m][2N], w*silu(a)*b -> dh [m][N], and the
 //          row's sums of u*silu(a)*b over each 64 columns -> dots [N/64][m_cap] when set
 enum Mode { kFc1 = 0, kFc2 = 1, kDgrad = 2, kFc1Q = 3, kDgradQ = 4 };
@@ -104,7 +105,9 @@ struct Epi {
   int N;   // output columns (fc1, dgrad: F; fc2: D)
   uint8_t* q;
   uint8_t* qs;
-  const float* rw;
+  const int32_t* src;
+  const float* tw;
+  int nslots;
   float* dots;
   int m_cap;
 };
@@ -199,6 +202,13 @@ __device__ __forceinline__ void quantize_run16(const f32x16& v, uint8_t* codes, 
   if (!writes) return;
   st16(codes, u32x4{w[0], w[1], w[2], w[3]});
   if (writes_scale) *scale = (uint8_t)sb;
+}
+
+// The weight of a token row.
+__device__ __forceinline__ float row_weight(const Epi& ep, int m) {
+  if (!ep.tw) return 1.0f;
+  const int s = ep.src[m];
+  return s >= 0 && s < ep.nslots ? ep.tw[s] : 0.0f;
 }
 
 // kDgradQ of one element: u the sum, a and b the checkpoint's values, w the row's weight.
@@ -709,7 +719,7 @@ __device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep,
     const bool in = r < t.rows, tok = r < t.vrows;
     const int m = t.m0 + r;
     const size_t row = (size_t)m * N;
-    const float w = !tok ? 0.0f : ep.rw ? ep.rw[m] : 1.0f;
+    const float w = tok ? row_weight(ep, m) : 0.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb) {
@@ -1312,11 +1322,24 @@ __device__ Tile decode_item(const Sched& sc, int E, int n_nt, int cols, int w) {
 // <= the workspace slots). Share sh of tail tile i is item full + sh*tail + i and writes
 // its float32 sums to workspace slot sh*tail + i; gg_tail_reduce adds the shares in
 // order sh = 0..S-1. Items [0, full) are whole tiles.
+//
+// min_saved: a tile is cut only if that saves at least so many k-steps of the round. The
+// 4-bit products and the checkpoint's two GEMMs ask for 12: writing, reading and adding
+// the shares costs 7 to 15 us, about 10 steps. (Measured with and without the split: fc1
+// on the checkpoint, 389 tokens top-2, D = 512 (5 steps saved) 32.9 against 25.6 us, D =
+// 1024 (10) 33.1 against 27.9, D = 2048 (21) 38.4 against 43.1; 4-bit fc2, 512 tokens top-2,
+// F = 2048 (5) 29.4 against 19.2 us, F = 8192 (21) 35.6 against 57.8.)
+constexpr int kMinSaved = 12;
+
 struct Split {
   int full, tail, S, nks;
 };
 
-__device__ Split split_plan(int total, int G, int slots, int nk) {
+constexpr int min_saved(int mode) { return mode >= kFc1Q ? kMinSaved : 0; }
+// Whether a GEMM of nk k-steps can cut its last round at all (at most 8 shares).
+constexpr bool may_split(int nk) { return nk - (nk + 7) / 8 >= kMinSaved; }
+
+__device__ Split split_plan(int total, int G, int slots, int nk, int min_saved) {
   Split p;
   const int rounds = (total + G - 1) / G;
   p.full = total;
@@ -1329,7 +1352,7 @@ __device__ Split split_plan(int total, int G, int slots, int nk) {
     int S = min(min(8, G / tail), min(slots / tail, nk));
     const int nks = (nk + S - 1) / S;
     S = (nk + nks - 1) / nks;   // no empty share
-    if (S >= 2) {
+    if (S >= 2 && nk - nks >= min_saved) {
       p.full = (rounds - 1) * G;
       p.tail = tail;
       p.S = S;
@@ -1356,7 +1379,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_bf16_kernel(
   const int n_nt = (N + cols - 1) / cols;
   const int total = sc.tstart[E] * n_nt;
   const int nk = K * EB / (BK * 2);   // 128-byte k-steps
-  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk);
+  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE));
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
   if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
@@ -1459,7 +1482,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_mx4_kernel(const bf16_t* __restric
   const int n_nt = (N + cols - 1) / cols;
   const int total = sc.tstart[E] * n_nt;
   const int nk = (KB + 127) / 128;
-  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk);
+  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, kMinSaved);
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
   if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
@@ -1692,7 +1715,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
   const int n_nt = (N + cols - 1) / cols;
   const int total = nblk * n_nt;
   const int nk = K / BK;
-  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk);
+  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE));
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
   if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
@@ -1766,14 +1789,14 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
 template <int MODE>
 __global__ __launch_bounds__(256) void gg_tail_reduce(Segs sg, int E, int K, int m_cap, int G,
                                                       int slots, const float* __restrict__ ws,
-                                                      Epi ep) {
+                                                      Epi ep, int min_saved) {
   constexpr bool FC1 = is_fc1(MODE);
   __shared__ Sched sc;
   build_sched(sc, sg, E, m_cap);
   const int N = ep.N;
   const int cols = FC1 ? BP / 2 : BP;
   const int n_nt = (N + cols - 1) / cols;
-  const Split sp = split_plan(sc.tstart[E] * n_nt, G, slots, K / BK);
+  const Split sp = split_plan(sc.tstart[E] * n_nt, G, slots, K / BK, min_saved);
   if (sp.tail == 0) return;
   constexpr int Q = (FC1 ? BP / 2 : BP) / 4;   // 4-column groups per row
   const int64_t units = (int64_t)sp.tail * BM * Q;
@@ -1827,7 +1850,7 @@ __global__ __launch_bounds__(256) void gg_tail_reduce(Segs sg, int E, int K, int
       const int m = t.m0 + r;
       const size_t row = (size_t)m * N;
       const bool tok = r < t.vrows;
-      const float w = !tok ? 0.0f : ep.rw ? ep.rw[m] : 1.0f;
+      const float w = tok ? row_weight(ep, m) : 0.0f;
       float va[4] = {0, 0, 0, 0}, vb[4] = {0, 0, 0, 0}, da[4], db[4], hw[4], dot = 0.0f;
       if (tok) {
         mx8_values4(*reinterpret_cast<const uint32_t*>(ep.q + 2 * row + n),
@@ -2274,7 +2297,7 @@ static hipError_t launch_mgrouped(int dt, int mode, bool p_mn, const void* A, Se
                          w1, w3, K, ep, ws, slots, MxScales{});
     if (slots)
       hipLaunchKernelGGL(gg_tail_reduce<kFc1>, rgrid, rblock, 0, s, sg, E, K, mc, G, slots,
-                         ws, ep);
+                         ws, ep, 0);
   } else if (mode == kFc2) {
     if (p_mn)
       hipLaunchKernelGGL((gg_bf16_kernel<kFc2, true>), grid, block, 0, s, a, sg, E, K, N, mc,
@@ -2287,13 +2310,13 @@ static hipError_t launch_mgrouped(int dt, int mode, bool p_mn, const void* A, Se
                          mc, w1, w1, K, ep, ws, slots, MxScales{});
     if (slots)
       hipLaunchKernelGGL(gg_tail_reduce<kFc2>, rgrid, rblock, 0, s, sg, E, K, mc, G, slots,
-                         ws, ep);
+                         ws, ep, 0);
   } else {
     hipLaunchKernelGGL((gg_bf16_kernel<kDgrad, true>), grid, block, 0, s, a, sg, E, K, N, mc,
                        w1, w1, K, ep, ws, slots, MxScales{});
     if (slots)
       hipLaunchKernelGGL(gg_tail_reduce<kDgrad>, rgrid, rblock, 0, s, sg, E, K, mc, G, slots,
-                         ws, ep);
+                         ws, ep, 0);
   }
   return hipGetLastError();
 }
@@ -2342,19 +2365,8 @@ hipError_t launch_grouped_fc1_mx(const void* xq_perm, const void* xs_perm,
   // are D / 128
   if (slots)
     hipLaunchKernelGGL(gg_tail_reduce<kFc1>, dim3(4 * G), dim3(256), 0, s, sg, E, D / 2,
-                       (int)m_cap, G, slots, ws, ep);
+                       (int)m_cap, G, slots, ws, ep, 0);
   return hipGetLastError();
-}
-
-// Each row's weight: its slot's top-k weight, 0 for rows without a slot.
-__global__ __launch_bounds__(256) void row_weight_kernel(const int32_t* __restrict__ src_row,
-                                                         const float* __restrict__ topk_w,
-                                                         int nslots, int m_cap,
-                                                         float* __restrict__ rw) {
-  const int r = blockIdx.x * 256 + threadIdx.x;
-  if (r >= m_cap) return;
-  const int s = src_row[r];
-  rw[r] = s >= 0 && s < nslots ? topk_w[s] : 0.0f;
 }
 
 // Each slot's sum of its row's partial sums, in column order; 0 for slots without a row.
@@ -2365,14 +2377,22 @@ __global__ __launch_bounds__(256) void row_dot_kernel(const int32_t* __restrict_
   const int s = blockIdx.x * 256 + threadIdx.x;
   if (s >= nslots) return;
   const int r = dst_row[s];
-  float sum = 0.0f;
-  if (r >= 0 && r < m_cap)
-    for (int p = 0; p < parts; ++p) sum += dots[(size_t)p * m_cap + r];
-  out[s] = sum;
+  float sum[8] = {};   // eight loads in flight; the order is fixed
+  if (r >= 0 && r < m_cap) {
+    const float* d = dots + r;
+    int p = 0;
+    for (; p + 8 <= parts; p += 8)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += d[(size_t)(p + i) * m_cap];
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (p + i < parts) sum[i] += d[(size_t)(p + i) * m_cap];
+  }
+  out[s] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
 }
 
 size_t ckpt8_scratch_bytes(int F, int64_t m_cap) {
-  return (size_t)m_cap * (1 + F / 64) * sizeof(float);
+  return (size_t)m_cap * (F / 64) * sizeof(float);
 }
 
 hipError_t launch_grouped_fc1_ckpt8(const void* x_perm, const int32_t* offsets,
@@ -2381,10 +2401,12 @@ hipError_t launch_grouped_fc1_ckpt8(const void* x_perm, const int32_t* offsets,
                                     void* workspace, size_t ws_bytes, hipStream_t s) {
   const int G = cu_count(), mc = (int)m_cap;
   float* ws = static_cast<float*>(workspace);
-  const int slots = ws ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20) : 0;
+  const int slots = ws && may_split(D / BK)
+                        ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20)
+                        : 0;
   const Segs sg{offsets, counts, 0};
   const Epi ep{static_cast<bf16_t*>(h), nullptr, nullptr, F, static_cast<uint8_t*>(q),
-               static_cast<uint8_t*>(qs), nullptr, nullptr, mc};
+               static_cast<uint8_t*>(qs), nullptr, nullptr, 0, nullptr, mc};
   const bf16_t* a = static_cast<const bf16_t*>(x_perm);
   const bf16_t *b1 = static_cast<const bf16_t*>(w1), *b3 = static_cast<const bf16_t*>(w3);
   if (use_ring(E, m_cap))
@@ -2395,7 +2417,7 @@ hipError_t launch_grouped_fc1_ckpt8(const void* x_perm, const int32_t* offsets,
                        mc, b1, b3, D, ep, ws, slots, MxScales{});
   if (slots)
     hipLaunchKernelGGL(gg_tail_reduce<kFc1Q>, dim3(4 * G), dim3(256), 0, s, sg, E, D, mc, G,
-                       slots, ws, ep);
+                       slots, ws, ep, kMinSaved);
   return hipGetLastError();
 }
 
@@ -2408,23 +2430,21 @@ hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offs
                                       size_t ws_bytes, hipStream_t s) {
   const int G = cu_count(), mc = (int)m_cap;
   float* ws = static_cast<float*>(workspace);
-  const int slots = ws ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20) : 0;
+  const int slots = ws && may_split(D / BK)
+                        ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20)
+                        : 0;
   const Segs sg{offsets, counts, 0};
-  float* rw = topk_w ? static_cast<float*>(scratch) : nullptr;
-  float* dots = dtopk_w ? static_cast<float*>(scratch) + m_cap : nullptr;
-  if (rw)
-    hipLaunchKernelGGL(row_weight_kernel, dim3((mc + 255) / 256), dim3(256), 0, s, src_row, topk_w,
-                       nslots, mc, rw);
+  float* dots = dtopk_w ? static_cast<float*>(scratch) : nullptr;
   const Epi ep{static_cast<bf16_t*>(dab), nullptr, static_cast<bf16_t*>(hw), F,
                static_cast<uint8_t*>(const_cast<void*>(q)),
-               static_cast<uint8_t*>(const_cast<void*>(qs)), rw, dots, mc};
+               static_cast<uint8_t*>(const_cast<void*>(qs)), src_row, topk_w, nslots, dots, mc};
   const bf16_t* w = static_cast<const bf16_t*>(w2);
   hipLaunchKernelGGL((gg_bf16_kernel<kDgradQ, true>), dim3(G), dim3(NTHR), 0, s,
                      static_cast<const bf16_t*>(dout_perm), sg, E, D, F, mc, w, w, D, ep, ws,
                      slots, MxScales{});
   if (slots)
     hipLaunchKernelGGL(gg_tail_reduce<kDgradQ>, dim3(4 * G), dim3(256), 0, s, sg, E, D, mc, G,
-                       slots, ws, ep);
+                       slots, ws, ep, kMinSaved);
   if (dtopk_w)
     hipLaunchKernelGGL(row_dot_kernel, dim3((nslots + 255) / 256), dim3(256), 0, s, dst_row, dots,
                        nslots, mc, F / 64, dtopk_w);
@@ -2437,7 +2457,10 @@ hipError_t launch_grouped_mx4(bool fc1, const void* aq, const void* as, const in
                               void* out, void* workspace, size_t ws_bytes, hipStream_t s) {
   const int G = cu_count();
   float* ws = static_cast<float*>(workspace);
-  const int slots = ws ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20) : 0;
+  const int nk = (K + 255) / 256;
+  const int slots = ws && may_split(nk)
+                        ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20)
+                        : 0;
   const Segs sg{offsets, counts, 0};
   const Epi ep{static_cast<bf16_t*>(out), nullptr, nullptr, N};
   const MxScales ms{static_cast<const uint32_t*>(as), static_cast<const uint32_t*>(w1s),
@@ -2446,12 +2469,10 @@ hipError_t launch_grouped_mx4(bool fc1, const void* aq, const void* as, const in
   hipLaunchKernelGGL(kern, dim3(G), dim3(NTHR), 0, s, static_cast<const bf16_t*>(aq), sg, E,
                      K / 2, N, (int)m_cap, static_cast<const bf16_t*>(w1q),
                      static_cast<const bf16_t*>(w3q), ep, ws, slots, ms);
-  // the reduction counts k-steps as K / 64 bf16 values: here a step is 256 values
-  const int kred = (K + 255) / 256 * 64;
-  if (slots) {
+  if (slots) {   // the reduction counts k-steps of 64 bf16 values
     const auto red = fc1 ? gg_tail_reduce<kFc1> : gg_tail_reduce<kFc2>;
-    hipLaunchKernelGGL(red, dim3(4 * G), dim3(256), 0, s, sg, E, kred, (int)m_cap, G, slots, ws,
-                       ep);
+    hipLaunchKernelGGL(red, dim3(4 * G), dim3(256), 0, s, sg, E, nk * BK, (int)m_cap, G, slots, ws,
+                       ep, kMinSaved);
   }
   return hipGetLastError();
 }

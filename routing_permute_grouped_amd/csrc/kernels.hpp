@@ -120,7 +120,7 @@ hipError_t launch_grouped_fc1_ckpt8(const void* x_perm, const int32_t* offsets,
                                     void* workspace, size_t ws_bytes, hipStream_t s);
 
 // its use in the backward: u = dout_perm w2[e] (unweighted rows), dab, hw = weighted h and,
-// when set, dtopk_w [nslots]; scratch (ckpt8_scratch_bytes) when topk_w is set
+// when set, dtopk_w [nslots], with scratch (ckpt8_scratch_bytes)
 size_t ckpt8_scratch_bytes(int F, int64_t m_cap);
 hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offsets,
                                       const int32_t* counts, int E, int D, int F, int64_t m_cap,

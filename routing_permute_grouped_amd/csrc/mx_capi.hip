@@ -173,16 +173,15 @@ moe_status_t moe_grouped_dgrad_swiglu_ckpt8(const void* dout_perm, const int32_t
   if (!aligned16(dout_perm) || !aligned16(w2) || !aligned16(ab_codes) || !ab_scales ||
       !aligned16(dab) || !aligned16(hw))
     return MOE_EINVAL;
-  if (topk_w && (!aligned4(topk_w) || !aligned4(src_row) || !aligned16(scratch)))
+  if (topk_w && (!aligned4(topk_w) || !aligned4(src_row))) return MOE_EINVAL;
+  if (dtopk_w &&
+      (!topk_w || !aligned4(dtopk_w) || !aligned4(dst_row) || !aligned16(scratch)))
     return MOE_EINVAL;
-  if (dtopk_w && (!topk_w || !aligned4(dtopk_w) || !aligned4(dst_row))) return MOE_EINVAL;
   const moe_status_t st =
       segments_ok(offsets, counts, tile_expert, E, D, F, m_tile, m_cap, workspace);
   if (st != MOE_OK) return st;
-  if (topk_w) {
-    if (!tk_ok(T, k) || k < 1 || k > kMaxK) return MOE_ESHAPE;
-    if (scratch_bytes < ckpt8_scratch_bytes(F, m_cap)) return MOE_EWORKSPACE;
-  }
+  if (topk_w && (!tk_ok(T, k) || k < 1 || k > kMaxK)) return MOE_ESHAPE;
+  if (dtopk_w && scratch_bytes < ckpt8_scratch_bytes(F, m_cap)) return MOE_EWORKSPACE;
   if (!workspace) ws_bytes = 0;
   return hip_status(launch_grouped_dgrad_ckpt8(
       dout_perm, offsets, counts, E, D, F, m_cap, w2, ab_codes, ab_scales, src_row, dst_row,

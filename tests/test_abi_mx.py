@@ -131,14 +131,14 @@ def use(d=FAKE, offs=FAKE, E=8, D=256, F=320, mt=16, m_cap=1024, w2=FAKE, q=FAKE
     (dict(hw=None), MOE_EINVAL), (dict(dab=FAKE + 8), MOE_EINVAL), (dict(src=None), MOE_EINVAL),
     (dict(scr=None), MOE_EINVAL), (dict(dst=None), MOE_EINVAL), (dict(tw=None), MOE_EINVAL),
     (dict(F=100), MOE_ESHAPE), (dict(T=0), MOE_ESHAPE), (dict(k=33), MOE_ESHAPE),
-    (dict(m_cap=1000), MOE_ECAPACITY), (dict(scrb=1024 * 4 * 6 - 1), MOE_EWORKSPACE),
+    (dict(m_cap=1000), MOE_ECAPACITY), (dict(scrb=1024 * 4 * 5 - 1), MOE_EWORKSPACE),
 ])
 def test_use_validation(kw, code):
     assert use(**kw) == code
 
 
 def test_scratch_bytes():
-    assert rpg.moe_ckpt8_scratch_bytes(320, 1024) == 1024 * 4 * 6
+    assert rpg.moe_ckpt8_scratch_bytes(320, 1024) == 1024 * 4 * 5
     assert rpg.moe_ckpt8_scratch_bytes(100, 1024) == 0
     assert rpg.moe_ckpt8_scratch_bytes(320, 0) == 0
 
