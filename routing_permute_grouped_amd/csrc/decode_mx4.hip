@@ -5,18 +5,26 @@
 //
 // Bound by the stream of the active experts' weights, 17/32 byte a value, a quarter of the
 // bf16 stream; per weight byte there is four times the work on the rows. Hence
-//   * a workgroup (4 waves) takes one expert; every row fragment read from LDS feeds two
-//     weight fragments: 16 columns of w1 and of w3 (fc1), or 32 columns of w2 (fc2);
+//   * a work item is 64 output columns for up to 64 rows of one expert; a workgroup of four
+//     waves takes one item after the other, each wave 16 of the columns: rows of w1 and of w3
+//     (fc1: one row fragment feeds both), or of w2;
 //   * a lane loads 16 bytes of a weight row: one whole MX block, so one scale serves them.
 //     Lane group g holds block g of a 128-value chunk, and its 8-code words are the four
 //     MFMA slices; the rows' fragments follow the same order (any order of k serves that
-//     both operands share);
+//     both operands share). One load brings KS chunks' scale words to the four lane groups,
+//     which exchange them by lane swaps: a byte load per chunk cost 12 to 15%;
 //   * v_cvt_scalef32_pk_bf16_fp4 turns two codes and the block's scale into two bf16
 //     values, exactly (one fraction bit, and a power of two), and v_mfma_f32_16x16x32_bf16
 //     multiplies;
 //   * rows come through LDS, KS chunks at a time, double-buffered through registers, one
-//     barrier per KS chunks; weights run PD groups ahead in registers. All loads are
-//     ordinary ones, so every wait is the compiler's own.
+//     barrier per KS chunks; weights run PD groups of KS chunks ahead in registers. All loads
+//     are ordinary ones, so every wait is the compiler's own;
+//   * four workgroups a CU hide the latency; deeper prefetch at three or two was slower (64
+//     experts of D = 2048, F = 1408, one row each: 57 us, at two workgroups and 16 chunks
+//     ahead 94), and so was splitting k over the waves (100 us);
+//   * the items that exist are found on the device from the counts, so that experts without
+//     rows and unused row groups cost no workgroup (one that looks up its count and leaves
+//     holds its place for more than a microsecond: 20 of 87 us with half of them empty).
 // Rows behind counts[e] are neither read nor written; an expert without rows reads nothing.
 #include <algorithm>
 
@@ -26,7 +34,10 @@
 namespace moe {
 namespace {
 
-constexpr int DW = 4;   // waves per workgroup
+constexpr int DW = 4;           // waves per workgroup
+constexpr int GROUP = 64;       // rows per workgroup
+constexpr int XBYTES = 32768;   // two row buffers: 16*NB rows of KS chunks (256 bytes) each
+constexpr int XCDS = 8;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
@@ -60,43 +71,72 @@ __device__ __forceinline__ void lds_barrier() {
 struct Mx4Weights {
   const uint8_t* q1;    // [E][N][K/2]
   const uint8_t* q2;    // fc1: w3's; fc2: w2's again
-  const uint8_t* s1;    // [K/128][E*N] words, as bytes
-  const uint8_t* s2;
+  const uint32_t* s1;   // [K/128][E*N] words
+  const uint32_t* s2;
 };
 
-// NB: row blocks of 16 of this workgroup's rows; KS: 128-value chunks per LDS buffer;
-// PD: groups of KS weight chunks in flight.
+// The scale words of KS chunks, held by the lane groups (group g: chunk g % KS), to byte g of
+// each chunk's word as a power of two: the swaps put group pairs, then halves, side by side.
+template <int KS>
+__device__ __forceinline__ void spread(uint32_t word, int g, float (&scale)[KS]) {
+  uint32_t w[4] = {word, word, word, word};
+  if (KS == 4) {
+    const auto h = __builtin_amdgcn_permlane32_swap(word, word, false, false);
+    w[0] = (uint32_t)h[0];
+    w[2] = (uint32_t)h[1];
+  }
+  if (KS >= 2) {
+    const auto a = __builtin_amdgcn_permlane16_swap(w[0], w[0], false, false);
+    w[0] = (uint32_t)a[0];
+    w[1] = (uint32_t)a[1];
+  }
+  if (KS == 4) {
+    const auto b = __builtin_amdgcn_permlane16_swap(w[2], w[2], false, false);
+    w[2] = (uint32_t)b[0];
+    w[3] = (uint32_t)b[1];
+  }
+#pragma unroll
+  for (int i = 0; i < KS; ++i)
+    scale[i] = __uint_as_float(__builtin_amdgcn_ubfe(w[i], 8 * g, 8) << 23);
+}
+
+// NB: row blocks of 16 of the item's rows; KS: 128-value chunks per LDS buffer; PD: groups of
+// KS weight chunks in flight. cols: the item's first column.
 template <bool FC1, int NB, int KS, int PD>
-__device__ __forceinline__ void dec4_body(char* xs, int xbytes, const bf16_t* __restrict__ X,
-                                          int e, int r0, int rows, int K, int N, int E,
+__device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X, int cols, int e,
+                                          int r0, int rows, int K, int N, int E,
                                           const Mx4Weights& wt, bf16_t* __restrict__ out) {
+  constexpr int NW = FC1 ? 2 : 1;                 // weight fragments a wave multiplies
   constexpr int ROWB = KS * 256;                  // bytes of a row's group of chunks
   constexpr int NX = NB * KS;                     // 16-byte units per thread and group
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  static_assert(2 * NB * 16 * ROWB <= XBYTES, "two row buffers");
+  // opaque per item, so that addresses derived from it are not kept across the items: with
+  // four bodies in the item loop they would not fit the registers
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 15, g = lane >> 4;
-  const int n0 = (blockIdx.x * DW + wave) * (FC1 ? 16 : 32);
+  const int n0 = cols + wave * 16;
   const int nch = K / 128;
   const int ngr = (nch + KS - 1) / KS;
 
-  // this lane's two weight rows and their scale bytes (byte g of a chunk's word)
-  const size_t row1 = (size_t)e * N + n0 + fr, row2 = FC1 ? row1 : row1 + 16;
-  const uint8_t* wrow[2] = {wt.q1 + row1 * (K / 2) + 16 * g,
-                            (FC1 ? wt.q2 : wt.q1) + row2 * (K / 2) + 16 * g};
-  const uint8_t* srow[2] = {wt.s1 + row1 * 4 + g, (FC1 ? wt.s2 : wt.s1) + row2 * 4 + g};
-  const size_t sstep = (size_t)E * N * 4;
-  u32x4 wr[PD][2][KS];
-  uint32_t sr[PD][2][KS];
-  // past the last chunk the last one is read again; its rows are zeros there
+  // this lane's weight rows, and their scale words of chunk g % KS of a group
+  const size_t row = (size_t)e * N + n0 + fr;
+  const uint8_t* wrow[2] = {wt.q1 + row * (K / 2) + 16 * g, wt.q2 + row * (K / 2) + 16 * g};
+  const uint32_t* srow[2] = {wt.s1 + row, wt.s2 + row};
+  const size_t sstep = (size_t)E * N;
+  u32x4 wr[PD][NW][KS];
+  uint32_t sr[PD][NW];
+  // past the last chunk of a group that K ends in, the last one again; its rows are zeros there
   auto wload = [&](int slot, int gr) {
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       const int c = min(gr * KS + i, nch - 1);
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        wr[slot][w][i] = ld16(wrow[w] + (size_t)c * 64);
-        sr[slot][w][i] = srow[w][c * sstep];
-      }
+      for (int w = 0; w < NW; ++w) wr[slot][w][i] = ld16(wrow[w] + (size_t)c * 64);
     }
+#pragma unroll
+    for (int w = 0; w < NW; ++w) sr[slot][w] = srow[w][min(gr * KS + g % KS, nch - 1) * sstep];
   };
 
   // unit q of a group: row q / (16*KS), 16-byte unit q % (16*KS) of the row's group
@@ -104,7 +144,7 @@ __device__ __forceinline__ void dec4_body(char* xs, int xbytes, const bf16_t* __
   auto xload = [&](int gr) {
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-      const int q = threadIdx.x + i * DW * 64;
+      const int q = tid + i * DW * 64;
       const int r = q / (16 * KS), u = q % (16 * KS);
       const int k0 = gr * (KS * 128) + u * 8;
       xr[i] = u32x4{0u, 0u, 0u, 0u};
@@ -115,37 +155,37 @@ __device__ __forceinline__ void dec4_body(char* xs, int xbytes, const bf16_t* __
   auto xstore = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-      const int q = threadIdx.x + i * DW * 64;
+      const int q = tid + i * DW * 64;
       const int r = q / (16 * KS), u = q % (16 * KS);
-      st16(xs + buf * xbytes + r * ROWB + ((u ^ (r & 15)) << 4), xr[i]);
+      st16(xs + buf * (XBYTES / 2) + r * ROWB + ((u ^ (r & 15)) << 4), xr[i]);
     }
   };
 
-  f32x4 acc[2][NB];
+  f32x4 acc[NW][NB];
 #pragma unroll
-  for (int w = 0; w < 2; ++w)
+  for (int w = 0; w < NW; ++w)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[w][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   auto compute = [&](int buf, int slot) {
-    const char* xb = xs + buf * xbytes;
+    const char* xb = xs + buf * (XBYTES / 2);
+    float scale[NW][KS];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) spread<KS>(sr[slot][w], g, scale[w]);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
-      float sc[2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) sc[w] = __uint_as_float(sr[slot][w][i] << 23);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        bf16x8 wf[2];
+        bf16x8 wf[NW];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) wf[w] = dequant8(wr[slot][w][i][s], sc[w]);
+        for (int w = 0; w < NW; ++w) wf[w] = dequant8(wr[slot][w][i][s], scale[w][i]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const int r = 16 * b + fr;
           const bf16x8 xf = __builtin_bit_cast(
               bf16x8, ld16(xb + r * ROWB + i * 256 + (((4 * g + s) ^ (r & 15)) << 4)));
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
+          for (int w = 0; w < NW; ++w)
             acc[w][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[w], xf, acc[w][b], 0, 0, 0);
         }
       }
@@ -154,7 +194,9 @@ __device__ __forceinline__ void dec4_body(char* xs, int xbytes, const bf16_t* __
 
   xload(0);
 #pragma unroll
-  for (int p = 0; p < PD; ++p) wload(p, p);
+  for (int p = 0; p < PD; ++p)
+    if (p < ngr) wload(p, p);
+  lds_barrier();   // the item before is done with the buffers
   xstore(0);
   xload(1);
   lds_barrier();
@@ -167,7 +209,7 @@ __device__ __forceinline__ void dec4_body(char* xs, int xbytes, const bf16_t* __
         // the other buffer's readers passed the barrier that ended the step before
         xstore((gr + 1) & 1);
         xload(gr + 2);
-        wload(j, gr + PD);
+        if (gr + PD < ngr) wload(j, gr + PD);
         lds_barrier();
       }
     }
@@ -179,73 +221,93 @@ __device__ __forceinline__ void dec4_body(char* xs, int xbytes, const bf16_t* __
     const int r = 16 * b + fr;
     if (r < rows) {
       bf16_t* p = out + ((size_t)r0 + r) * N + n0 + 4 * g;
-      const f32x4 &a = acc[0][b], &u = acc[1][b];
-      if (FC1) {
+      const f32x4 &a = acc[0][b], &u = acc[NW - 1][b];
+      if (FC1)
         store4(p, silu_mul(a[0], u[0]), silu_mul(a[1], u[1]), silu_mul(a[2], u[2]),
                silu_mul(a[3], u[3]));
-      } else {
+      else
         store4(p, a[0], a[1], a[2], a[3]);
-        store4(p + 16, u[0], u[1], u[2], u[3]);
-      }
     }
   }
 }
 
-// One workgroup per (64 fc1 or 128 fc2 columns, expert, 16*TB of its rows). The body is
-// chosen by the rows that are there.
-template <bool FC1, int TB, int KS, int PD>
-__global__ __launch_bounds__(DW * 64) void dec4_kernel(const bf16_t* __restrict__ X,
-                                                       const int32_t* __restrict__ counts,
-                                                       int cap, int K, int N, Mx4Weights wt,
-                                                       bf16_t* __restrict__ out) {
-  constexpr int XBYTES = TB * 16 * KS * 256;
-  __shared__ __attribute__((aligned(1024))) char xs[2 * XBYTES];
-  const int e = blockIdx.y;
-  const int first = blockIdx.z * (16 * TB);
-  const int rows = min(max(0, min(counts[e], cap)) - first, 16 * TB);
-  if (rows <= 0) return;   // uniform over the workgroup: the weights stay unread
-  const int r0 = e * cap + first;
-#define DEC4_CASE(n)                                                                          \
-  case n:                                                                                     \
-    if (TB >= n)                                                                              \
-      dec4_body<FC1, (TB >= n ? n : 1), KS, PD>(xs, XBYTES, X, e, r0, rows, K, N, gridDim.y,  \
-                                                wt, out);                                     \
-    break;
-  switch ((rows + 15) >> 4) {
-    DEC4_CASE(1)
-    DEC4_CASE(2)
-    DEC4_CASE(3)
-    DEC4_CASE(4)
-    DEC4_CASE(5)
-    DEC4_CASE(6)
-    DEC4_CASE(7)
-    default:
-      if (TB >= 8)
-        dec4_body<FC1, (TB >= 8 ? 8 : 1), KS, PD>(xs, XBYTES, X, e, r0, rows, K, N, gridDim.y,
-                                                  wt, out);
-      break;
+// Row groups of 64 of expert e (none past the last expert).
+__device__ __forceinline__ int row_groups(const int32_t* counts, int e, int E, int cap) {
+  return e < E ? (max(0, min(counts[e], cap)) + GROUP - 1) / GROUP : 0;
+}
+
+// Exclusive prefix sum over the wave; total: the whole sum.
+__device__ __forceinline__ int wave_scan(int v, int& total) {
+  const int lane = threadIdx.x & 63;
+  int inc = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
   }
-#undef DEC4_CASE
+  total = __builtin_amdgcn_readlane(inc, 63);
+  return inc - v;
+}
+
+// The last lane whose prefix sum is not past v.
+__device__ __forceinline__ int last_lane(int prefix, bool in, int v) {
+  return 63 - __clzll(__ballot(in && prefix <= v));
+}
+
+// Every wave holds the row groups' prefix sums over the experts, `per` experts a lane, and
+// numbers the items expert by expert: expert e, whose groups start at s, owns items
+// [s, s + its groups) * ncols. Of one expert's items, the row groups of eight column blocks
+// follow each other at a distance of eight, so those of one column block run on one XCD,
+// close in time, and the second finds the weights in its L2.
+template <bool FC1>
+__global__ __launch_bounds__(DW * 64, 4) void dec4_kernel(const bf16_t* __restrict__ X,
+                                                          const int32_t* __restrict__ counts,
+                                                          int cap, int E, int K, int N,
+                                                          Mx4Weights wt,
+                                                          bf16_t* __restrict__ out) {
+  __shared__ __attribute__((aligned(1024))) char xs[XBYTES];
+  const int lane = threadIdx.x & 63;
+  const int per = (E + 63) / 64, ncols = N / 64;
+  int sum = 0, groups;
+  for (int i = 0; i < per; ++i) sum += row_groups(counts, lane * per + i, E, cap);
+  const int start = wave_scan(sum, groups);
+  const int items = groups * ncols;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int grp = item / ncols;
+    int e = last_lane(start, true, grp);
+    int s = __builtin_amdgcn_readlane(start, e);
+    if (per > 1) {   // the lane's experts, one a lane
+      int all;
+      const int at = wave_scan(lane < per ? row_groups(counts, e * per + lane, E, cap) : 0, all);
+      const int l = last_lane(at, lane < per, grp - s);
+      s += __builtin_amdgcn_readlane(at, l);
+      e = e * per + l;
+    }
+    const int n = max(0, min(counts[e], cap)), ng = (n + GROUP - 1) / GROUP;
+    const int local = item - s * ncols;
+    const int base = local / (XCDS * ng) * XCDS, in = local - base * ng;
+    const int width = min(XCDS, ncols - base);
+    const int first = in / width * GROUP, cols = (base + in % width) * 64;
+    const int rows = min(n - first, GROUP), r0 = e * cap + first;
+    if (rows <= 16)
+      dec4_body<FC1, 1, 4, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+    else if (rows <= 32)
+      dec4_body<FC1, 2, 2, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+    else if (rows <= 48)
+      dec4_body<FC1, 3, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+    else
+      dec4_body<FC1, 4, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+  }
 }
 
 template <bool FC1>
 void launch_dec4(const void* X, const int32_t* counts, int cap, int E, int K, int N,
                  const Mx4Weights& wt, void* out, hipStream_t s) {
-  const int cols = FC1 ? 64 : 128;
-  const bf16_t* x = static_cast<const bf16_t*>(X);
-  bf16_t* o = static_cast<bf16_t*>(out);
-  const auto go = [&](auto kern, int tb) {
-    const dim3 grid(N / cols, E, (cap + 16 * tb - 1) / (16 * tb));
-    hipLaunchKernelGGL(kern, grid, dim3(DW * 64), 0, s, x, counts, cap, K, N, wt, o);
-  };
-  if (cap <= 16)
-    go(dec4_kernel<FC1, 1, 4, 2>, 1);
-  else if (cap <= 32)
-    go(dec4_kernel<FC1, 2, 4, 2>, 2);
-  else if (cap <= 64)
-    go(dec4_kernel<FC1, 4, 2, 2>, 4);
-  else
-    go(dec4_kernel<FC1, 8, 2, 2>, 8);
+  const int64_t most = (int64_t)E * ((cap + GROUP - 1) / GROUP) * (N / 64);
+  const int grid = (int)std::min<int64_t>(4 * cu_count(), most);
+  hipLaunchKernelGGL(dec4_kernel<FC1>, dim3(grid), dim3(DW * 64), 0, s,
+                     static_cast<const bf16_t*>(X), counts, cap, E, K, N, wt,
+                     static_cast<bf16_t*>(out));
 }
 
 }  // namespace
@@ -253,9 +315,10 @@ void launch_dec4(const void* X, const int32_t* counts, int cap, int E, int K, in
 hipError_t launch_decode_mx4(const void* x, const int32_t* counts, int E, int D, int F, int cap,
                              const void* w1q, const void* w1s, const void* w3q, const void* w3s,
                              const void* w2q, const void* w2s, void* h, void* y, hipStream_t s) {
-  const auto b = [](const void* p) { return static_cast<const uint8_t*>(p); };
-  launch_dec4<true>(x, counts, cap, E, D, F, Mx4Weights{b(w1q), b(w3q), b(w1s), b(w3s)}, h, s);
-  launch_dec4<false>(h, counts, cap, E, F, D, Mx4Weights{b(w2q), b(w2q), b(w2s), b(w2s)}, y, s);
+  const auto q = [](const void* p) { return static_cast<const uint8_t*>(p); };
+  const auto w = [](const void* p) { return static_cast<const uint32_t*>(p); };
+  launch_dec4<true>(x, counts, cap, E, D, F, Mx4Weights{q(w1q), q(w3q), w(w1s), w(w3s)}, h, s);
+  launch_dec4<false>(h, counts, cap, E, F, D, Mx4Weights{q(w2q), q(w2q), w(w2s), w(w2s)}, y, s);
   return hipGetLastError();
 }
 
