@@ -119,6 +119,7 @@ moe_status_t moe_grouped_swiglu_masked_mxfp4(const void* x_masked, const int32_t
  *   -> h [m_cap,F] bf16, bit for bit moe_grouped_fc1_swiglu's without a workspace (with one
  *                    the two calls may cut different tiles over k: another order of sums)
  *      ab_codes [m_cap,2F] e4m3 codes of [a | b], ab_scales [m_cap,2F/32] bytes
+ *                    (4-byte aligned)
  * Blocks are 32 consecutive columns of a or of b, quantised from the float32 sums. Pad rows
  * give exact zeros. Per row 2F*33/32 bytes in place of 4F. Arguments otherwise, workspace
  * and errors as moe_grouped_fc1_swiglu.

@@ -169,9 +169,23 @@ __device__ __forceinline__ void run_to_groups(uint32_t (&w)[4]) {
   swap_halves(w[1], w[3]);
 }
 
-// The lane's 16 values of a block row (by groups), rounded to bf16, to 32 bytes at p: its
-// run. Every lane takes part in the exchange; `writes` lanes store.
-__device__ __forceinline__ void run16_out(bf16_t* p, const float (&v)[16], bool writes) {
+// The epilogues' memory side: raw buffers over a tile's rows, so rows past the tile are not
+// stored and rows past its tokens read as zeros with no branch around an access. (With the
+// accesses under branches the compiler kept each block's loads behind the block before:
+// 230 us of epilogue in 569 us, 138 of them waiting for the codes.) The whole offset is
+// the lane's, the scalar one 0, for two reasons: the hardware compares the lane's offset with
+// the size less the scalar offset, without a sign, so that a scalar offset past the size would
+// let every lane through; and a 16-byte store with a scalar offset register was seen to take
+// its data's successor when the next instruction wrote the register (lanes 12-15 and 28-31
+// stored it now and then): the compiler puts a wait between the two only without one.
+typedef __amdgpu_buffer_rsrc_t rows_t;
+__device__ __forceinline__ rows_t tile_rows(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
+}
+
+// The lane's 16 values of a block row (by groups), rounded to bf16, to the 32 bytes at off:
+// its run.
+__device__ __forceinline__ void run16_out(rows_t rows, int off, const float (&v)[16]) {
   uint32_t lo[4], hi[4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -180,15 +194,13 @@ __device__ __forceinline__ void run16_out(bf16_t* p, const float (&v)[16], bool 
   }
   groups_to_run(lo);
   groups_to_run(hi);
-  if (!writes) return;
-  st16(p, u32x4{lo[0], hi[0], lo[1], hi[1]});
-  st16(p + 8, u32x4{lo[2], hi[2], lo[3], hi[3]});
+  __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, rows, off, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[2], hi[2], lo[3], hi[3]}, rows, off + 16, 0, 0);
 }
 
-// The lane's 16 sums of one block row, quantised: the run's codes and, from the lanes that
-// write it, the block's byte.
-__device__ __forceinline__ void quantize_run16(const f32x16& v, uint8_t* codes, uint8_t* scale,
-                                               bool writes_scale, bool writes) {
+// The lane's 16 sums of one block row, quantised: the run's codes stored; returns the block's
+// byte.
+__device__ __forceinline__ uint32_t quantize_run16(const f32x16& v, rows_t rows, int off) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
@@ -199,9 +211,8 @@ __device__ __forceinline__ void quantize_run16(const f32x16& v, uint8_t* codes, 
   for (int g = 0; g < 4; ++g)
     w[g] = mx8_codes4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3], sb);
   groups_to_run(w);
-  if (!writes) return;
-  st16(codes, u32x4{w[0], w[1], w[2], w[3]});
-  if (writes_scale) *scale = (uint8_t)sb;
+  __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, rows, off, 0, 0);
+  return sb;
 }
 
 // The weight of a token row.
@@ -681,60 +692,117 @@ template <bool HALF>
 __device__ __forceinline__ void fc1q_epilogue(const Tile& t, const Epi& ep,
                                               const f32x16 (&acc)[HALF ? 2 : 4][2]) {
   constexpr int WM = HALF ? 2 : 4;
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int wave = threadIdx.x >> 6;
-  const int n = t.n0 + (wave >> 1) * 32;
-  if (n >= ep.N) return;   // N is a multiple of 64: a block of 32 columns is in or out
+  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = ep.N, n = t.n0 + (wave >> 1) * 32;
+  if (n >= N) return;   // N is a multiple of 64: a block of 32 columns is in or out
+  const size_t m0 = t.m0;
+  const rows_t rq = tile_rows(ep.q + m0 * 2 * N, t.rows * 2 * N);
+  const rows_t rs = tile_rows(ep.qs + m0 * (N / 16), t.rows * (N / 16));
+  const rows_t rh = tile_rows(ep.C + m0 * N, t.rows * N * 2);
+  const int oq = fr * 2 * N + 16 * half, oh = (fr * N + 16 * half) * 2;
+  const int os = fr * (N / 16) + half * (N / 32);   // half 0 stores a's byte, half 1 b's
 #pragma unroll
   for (int mb = 0; mb < WM; ++mb) {
-    const int r = (wave & 1) * (HALF ? 64 : 128) + mb * 32 + (lane & 31);
-    const bool in = r < t.rows;
-    const size_t row = (size_t)(t.m0 + r) * ep.N;
+    const int r = (wave & 1) * (HALF ? 64 : 128) + mb * 32;
     const f32x16 &a = acc[mb][0], &b = acc[mb][1];
-    uint8_t* qs = ep.qs + row / 16 + n / 32;   // 2N/32 bytes a row
-    quantize_run16(a, ep.q + 2 * row + n + 16 * half, qs, half == 0, in);
-    quantize_run16(b, ep.q + 2 * row + ep.N + n + 16 * half, qs + ep.N / 32, half == 1, in);
+    const uint32_t sa = quantize_run16(a, rq, oq + (r * 2 * N + n));
+    const uint32_t sb = quantize_run16(b, rq, oq + (r * 2 * N + N + n));
+    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(half ? sb : sa), rs,
+                                         os + (r * (N / 16) + n / 32), 0, 0);
     float h[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) h[i] = silu_mul(a[i], b[i]);
-    run16_out(ep.C + row + n + 16 * half, h, in);
+    run16_out(rh, oh + (r * N + n) * 2, h);
   }
 }
 
 // kDgradQ epilogue, straight from the accumulators: per row, the wave's two blocks of 32
-// columns with their codes (16 bytes of a and of b a lane) and scales. The products of a
-// row's 64 columns are summed in the lane, then over the two lane halves.
+// columns with their codes (16 bytes of a and of b a lane) and scales, read one block of rows
+// ahead. The products of a row's 64 columns are summed in the lane, then over the two lane
+// halves. About 100 cycles of vector arithmetic an element of the wave, 32 of them in the
+// sigmoid's exponential and reciprocal: 11 us of a full tile, against 60 for its 32 k-steps.
+//
+// Slots: the slots of the wave's rows, one or two a lane, asked for before the main loop so
+// that only the weights' own load is left to wait for here.
+struct Slots {
+  int s[2];
+};
 template <bool HALF>
-__device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep,
+__device__ __forceinline__ Slots wave_slots(const Tile& t, const Epi& ep) {
+  const int r = (int)((threadIdx.x >> 6) & 1) * (HALF ? 64 : 128) + (int)(threadIdx.x & 63);
+  Slots o{{-1, -1}};
+  if (ep.tw) {   // uniform
+    const rows_t rr = tile_rows(ep.src + t.m0, t.vrows * 4);   // rows past the tokens get weight 0
+    o.s[0] = (int)__builtin_amdgcn_raw_buffer_load_b32(rr, r * 4, 0, 0);
+    if (!HALF) o.s[1] = (int)__builtin_amdgcn_raw_buffer_load_b32(rr, r * 4 + 256, 0, 0);
+  }
+  return o;
+}
+template <bool HALF>
+__device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep, const Slots& slots,
                                                 const f32x16 (&acc)[HALF ? 2 : 4][2]) {
   constexpr int WM = HALF ? 2 : 4;
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int wave = threadIdx.x >> 6;
-  const int n0 = t.n0 + (wave >> 1) * 64;
-  const int N = ep.N;
+  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = ep.N, n0 = t.n0 + (wave >> 1) * 64;
   if (n0 >= N) return;   // N is a multiple of 64
+  const size_t m0 = t.m0;
+  const rows_t rq = tile_rows(ep.q + m0 * 2 * N, t.vrows * 2 * N);
+  const rows_t rs = tile_rows(ep.qs + m0 * (N / 16), t.vrows * (N / 16));
+  const rows_t rc = tile_rows(ep.C + m0 * 2 * N, t.rows * 4 * N);
+  const rows_t rh = tile_rows(ep.dh + m0 * N, t.rows * 2 * N);
+  const int w0 = (wave & 1) * (HALF ? 64 : 128);   // the wave's first row
+  const int oq = fr * 2 * N + 16 * half, os = fr * (N / 16), oc = 2 * oq;
+  const int oh = (fr * N + 16 * half) * 2;
+
+  struct Block {   // pad rows: a = b = 0 and u = 0 give zeros
+    u32x4 a[2], b[2];
+    uint32_t sa, sb;   // the two blocks' scale bytes
+  };
+  auto load = [&](int mb) {
+    const int r = w0 + 32 * mb;
+    Block k;
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) {
+      const int off = oq + (r * 2 * N + n0 + 32 * nb);
+      k.a[nb] = __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0);
+      k.b[nb] = __builtin_amdgcn_raw_buffer_load_b128(rq, off + N, 0, 0);
+    }
+    const int off = os + (r * (N / 16) + n0 / 32);
+    k.sa = __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0);
+    k.sb = __builtin_amdgcn_raw_buffer_load_b16(rs, off + N / 32, 0, 0);
+    return k;
+  };
+  Block next = load(0);
+  // lane l: the weights of rows w0 + l and w0 + 64 + l, 0 without a slot or a token
+  float wl[2] = {1.0f, 1.0f};
+#pragma unroll
+  for (int i = 0; i < (HALF ? 1 : 2); ++i) {
+    const int sl = slots.s[i];
+    const bool in = sl >= 0 && sl < ep.nslots;
+    if (ep.tw) {
+      const float v = ep.tw[in ? sl : 0];
+      wl[i] = in ? v : 0.0f;
+    }
+    if (w0 + 64 * i + lane >= t.vrows) wl[i] = 0.0f;
+  }
+  float* dots = ep.dots ? ep.dots + (size_t)(n0 >> 6) * ep.m_cap + m0 : nullptr;
 #pragma unroll
   for (int mb = 0; mb < WM; ++mb) {
-    const int r = (wave & 1) * (HALF ? 64 : 128) + mb * 32 + (lane & 31);
-    const bool in = r < t.rows, tok = r < t.vrows;
-    const int m = t.m0 + r;
-    const size_t row = (size_t)m * N;
-    const float w = tok ? row_weight(ep, m) : 0.0f;
+    const int r = w0 + 32 * mb;
+    const Block k = next;
+    const float w = __shfl(wl[mb >> 1], 32 * (mb & 1) + fr);
+    if (mb + 1 < WM) next = load(mb + 1);
     float dot = 0.0f;
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb) {
       const int n = n0 + 32 * nb;
-      u32x4 ca = {0u, 0u, 0u, 0u}, cb = {0u, 0u, 0u, 0u};
-      uint32_t sa = 0u, sb = 0u;   // pad rows: a = b = 0 and u = 0 give zeros
-      if (tok) {
-        ca = ld16(ep.q + 2 * row + n + 16 * half);
-        cb = ld16(ep.q + 2 * row + N + n + 16 * half);
-        sa = ep.qs[row / 16 + n / 32];
-        sb = ep.qs[row / 16 + N / 32 + n / 32];
-      }
-      uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+      uint32_t wa[4] = {k.a[nb].x, k.a[nb].y, k.a[nb].z, k.a[nb].w};
+      uint32_t wb[4] = {k.b[nb].x, k.b[nb].y, k.b[nb].z, k.b[nb].w};
       run_to_groups(wa);
       run_to_groups(wb);
+      const uint32_t sa = (k.sa >> (8 * nb)) & 255u, sb = (k.sb >> (8 * nb)) & 255u;
       float da[16], db[16], hw[16];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -750,12 +818,14 @@ __device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep,
           dot += d.dot;
         }
       }
-      run16_out(ep.C + 2 * row + n + 16 * half, da, in);
-      run16_out(ep.C + 2 * row + N + n + 16 * half, db, in);
-      run16_out(ep.dh + row + n + 16 * half, hw, in);
+      run16_out(rc, oc + (r * 2 * N + n) * 2, da);
+      run16_out(rc, oc + (r * 2 * N + N + n) * 2, db);
+      run16_out(rh, oh + (r * N + n) * 2, hw);
+      // keeps the later blocks' arithmetic out of the registers
+      __builtin_amdgcn_sched_barrier(0);
     }
     dot += __shfl_xor(dot, 32);
-    if (ep.dots && in && half == 0) ep.dots[(size_t)(n0 >> 6) * ep.m_cap + m] = dot;
+    if (dots && half == 0 && r + fr < t.rows) dots[r + fr] = dot;
   }
 }
 
@@ -768,7 +838,8 @@ template <int MODE, bool HALF>
 __device__ __forceinline__ void finish_tile(char* smem, const Tile& t, const Epi& ep, int kb,
                                             int ke, float* __restrict__ part, int stage0,
                                             const f32x16 (&acc)[HALF ? 2 : 4][2],
-                                            char* elo = nullptr, char* ehi = nullptr) {
+                                            char* elo = nullptr, char* ehi = nullptr,
+                                            const Slots& slots = Slots{}) {
   constexpr int WM = HALF ? 2 : 4;
   constexpr int WN = 2;
   const int lane = threadIdx.x & 63;
@@ -806,7 +877,7 @@ __device__ __forceinline__ void finish_tile(char* smem, const Tile& t, const Epi
     return;
   }
   if (MODE == kDgradQ) {
-    dgradq_epilogue<HALF>(t, ep, acc);
+    dgradq_epilogue<HALF>(t, ep, slots, acc);
     return;
   }
 #pragma unroll
@@ -849,9 +920,11 @@ __device__ __forceinline__ void run_tile(char* smem, const Tile& t, const TileLo
                                          float* __restrict__ part, int stage0, bool primed,
                                          const TileLoads& nxt, bool has_next, int nkb) {
   f32x16 acc[HALF ? 2 : 4][2];
+  Slots slots{};
+  if (MODE == kDgradQ) slots = wave_slots<HALF>(t, ep);
   mainloop<HALF, false, P_MN, GUARD>(smem, ld, kb, ke, stage0, primed, nxt, has_next, nkb, acc,
                                      t.vrows);
-  finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc);
+  finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc, nullptr, nullptr, slots);
 }
 
 // ---------------------------------------------------------------------------

@@ -145,7 +145,7 @@ moe_status_t moe_grouped_fc1_swiglu_ckpt8(const void* x_perm, const int32_t* off
                                           void* ab_codes, void* ab_scales, void* workspace,
                                           size_t ws_bytes, void* stream) {
   if (!aligned16(x_perm) || !aligned16(w1) || !aligned16(w3) || !aligned16(h) ||
-      !aligned16(ab_codes) || !ab_scales)
+      !aligned16(ab_codes) || !aligned4(ab_scales))
     return MOE_EINVAL;
   const moe_status_t st =
       segments_ok(offsets, counts, tile_expert, E, D, F, m_tile, m_cap, workspace);
@@ -170,8 +170,8 @@ moe_status_t moe_grouped_dgrad_swiglu_ckpt8(const void* dout_perm, const int32_t
                                             int k, void* dab, void* hw, float* dtopk_w,
                                             void* scratch, size_t scratch_bytes,
                                             void* workspace, size_t ws_bytes, void* stream) {
-  if (!aligned16(dout_perm) || !aligned16(w2) || !aligned16(ab_codes) || !ab_scales ||
-      !aligned16(dab) || !aligned16(hw))
+  if (!aligned16(dout_perm) || !aligned16(w2) || !aligned16(ab_codes) ||
+      !aligned4(ab_scales) || !aligned16(dab) || !aligned16(hw))
     return MOE_EINVAL;
   if (topk_w && (!aligned4(topk_w) || !aligned4(src_row))) return MOE_EINVAL;
   if (dtopk_w &&

@@ -111,7 +111,8 @@ def save(x=FAKE, offs=FAKE, E=8, D=256, F=320, mt=16, m_cap=1024, w=FAKE, h=FAKE
 
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), MOE_EINVAL), (dict(w=FAKE + 4), MOE_EINVAL), (dict(h=None), MOE_EINVAL),
-    (dict(q=FAKE + 8), MOE_EINVAL), (dict(s=None), MOE_EINVAL), (dict(offs=FAKE + 1), MOE_EINVAL),
+    (dict(q=FAKE + 8), MOE_EINVAL), (dict(s=None), MOE_EINVAL), (dict(s=FAKE + 2), MOE_EINVAL),
+    (dict(offs=FAKE + 1), MOE_EINVAL),
     (dict(ws=FAKE + 8, wsb=1), MOE_EINVAL), (dict(D=100), MOE_ESHAPE), (dict(F=96), MOE_ESHAPE),
     (dict(E=0), MOE_ESHAPE), (dict(m_cap=1000), MOE_ECAPACITY),
 ])
