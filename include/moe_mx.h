@@ -74,8 +74,8 @@ moe_status_t moe_permute_mxfp4(const void* xq, const void* xs, const int32_t* to
  *   fc1: xq_perm [m_cap,D/2], w1q, w3q [E,F,D/2]
  *        -> h [m_cap,F] = silu(x w1[e]^T) * (x w3[e]^T) per segment row
  *   fc2: hq [m_cap,F/2], w2q [E,D,F/2] -> y_perm [m_cap,D] = h w2[e]^T per segment row
- * Scales in MOE_MX_KSTEPS: the rows' over m_cap rows, the weights' over their E*F (fc2: E*D)
- * rows. Segments, counts, tile_expert, m_tile and the optional workspace as
+ * Scales in MOE_MX_KSTEPS, 16-byte aligned: the rows' over m_cap rows, the weights' over their
+ * E*F (fc2: E*D) rows. Segments, counts, tile_expert, m_tile and the optional workspace as
  * moe_grouped_swiglu: with counts, pad rows are not read and give exact zeros; rows at or
  * past offsets[E] are neither read nor written. fc1: D a multiple of 128, F of 64; fc2: F a
  * multiple of 128, D of 64; D*F < 2^31. Every m_tile.

@@ -36,6 +36,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "kernels.hpp"
@@ -1133,47 +1134,51 @@ __device__ __forceinline__ void run_tile_mx(char* smem, const Tile& t, const Epi
 // the low half) with one E8M0 scale per 32 values along K, on
 // v_mfma_scale_f32_32x32x64_f8f6f4 with both operands FP4 (four operand registers and
 // half the FP8 cycles). A k-step is 256 k: 128-byte LDS rows again, so the stages, the
-// swizzle, the load pattern and the epilogues are the bf16 kernel's, and per byte moved
-// the matrix cores do what they do there. Lane half h of slice ks reads chunk 2*ks + h of
-// its row, 32 codes that are exactly one MX block, with that block's scale byte. K is a
-// multiple of 128; with an odd number of 128-value words the last step runs two slices,
-// and what its loads brought from past the row's end (the next row, or zeros) is not read.
+// swizzle and the load pattern are the bf16 kernel's, and per byte moved the matrix cores
+// do what they do there. Lane half h of slice ks reads chunk 2*ks + h of its row, 32 codes
+// that are exactly one MX block, with that block's scale byte. K is a multiple of 128; with
+// an odd number of 128-value words the last step runs two slices, and what its loads
+// brought from past the row's end (the next row, or zeros) is not read.
+//
+// What the pipeline adds to the bf16 kernel's:
+//   * a step's scale words come by direct loads too, six 1 KiB pieces (four for fc2) of one
+//     word of 256 rows each, one a wave, into LDS behind the stage. As loads into the
+//     registers of every wave that needs them (six a wave and step) they cost 6 to 19%;
+//   * the epilogue stores straight from the accumulators, without branches, so that a wave's
+//     stores are a known number and the next tile's first step can wait for its loads, which
+//     are older, and leave the stores in flight.
 // ---------------------------------------------------------------------------
+constexpr int MX4_SCALES = 6 * 1024;   // bytes of one stage's scale words
 
-// Raw scale words of step kt for this wave: lane half h holds word 2*kt + h of its row
-// (the last word again where the row has none). Rows past the token rows get zero words:
-// their codes are zeros, and a zero word cannot turn those into NaN.
-template <bool FC1, bool HALF>
-__device__ __forceinline__ void mx4_scale_words(const Tile& t, const MxScales& ms, int E, int N,
-                                                int nkw, int kt, uint32_t (&sa)[HALF ? 2 : 4],
-                                                uint32_t (&sw)[2]) {
-  constexpr int WM = HALF ? 2 : 4;
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int arow0 = (wave & 1) * (HALF ? 64 : 128);
-  const int prow0 = (wave >> 1) * 64;
-  const int fr = lane & 31;
-  const int s = min(2 * kt + (lane >> 5), nkw - 1);
-  const uint32_t* a = ms.a + (size_t)s * ms.ra + t.m0;
-#pragma unroll
-  for (int mb = 0; mb < WM; ++mb) {
-    const int r = arow0 + mb * 32 + fr;
-    sa[mb] = r < t.vrows ? a[r] : 0u;
+struct Mx4Src {
+  const bf16_t* A;
+  const bf16_t* W1;
+  const bf16_t* W3;
+  MxScales ms;
+  int KB, N, E;   // bytes of a row (K / 2), panel rows of an expert, experts
+  template <bool FC1>
+  __device__ TileLoads loads(const Tile& t) const {
+    return tile_loads<FC1, false, 1>(t, A, W1, W3, KB, N, KB);
   }
-  const size_t w0 = (size_t)s * E * N + (size_t)t.e * N;
-  if (FC1) {   // the wave's panel blocks are the w1 and w3 rows of the same columns
-    const size_t r = w0 + min(t.n0 + prow0 / 2 + fr, N - 1);
-    sw[0] = ms.w1[r];
-    sw[1] = ms.w3[r];
-  } else {
-    sw[0] = ms.w1[w0 + min(t.n0 + prow0 + fr, N - 1)];
-    sw[1] = ms.w1[w0 + min(t.n0 + prow0 + 32 + fr, N - 1)];
+  // Wave w's piece of step kt's scale words, to LDS address `lds` + 1024*w: word w % 2 of the
+  // step, of the rows of A (w / 2 = 0), of the panel's w1 (or w2) rows (1), of its w3 rows (2).
+  // Rows past the token rows get zero words (their codes are zeros, and a zero word cannot
+  // turn those into NaN), and so does a word past the row's last.
+  template <bool FC1>
+  __device__ void issue_scales(const Tile& t, int kt, uint32_t lds) const {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kind = wave >> 1, s = 2 * kt + (wave & 1);
+    if (kind >= (FC1 ? 3 : 2)) return;
+    const uint32_t* p = kind == 0 ? ms.a + (size_t)s * ms.ra + t.m0
+                                  : (kind == 1 ? ms.w1 : ms.w3) + ((size_t)s * E + t.e) * N + t.n0;
+    const int rows = s < KB / 64 ? (kind == 0 ? t.vrows : min(N - t.n0, BP)) : 0;
+    dma16(buffer_rsrc(p, (uint32_t)rows * 4u), (threadIdx.x & 63) * 16, 0, lds + wave * 1024);
   }
-}
+};
 
-// Raw words to the two the MFMAs take: word j of the step in every lane, its bytes moved
-// down by the lane half, so that op_sel byte 0 (even slice) or 2 (odd slice) is the byte
-// of the half's own block.
+// A lane's raw scale word, word lane/32 of the step, to the two words the MFMAs take, their
+// bytes moved down by the lane half, so that op_sel byte 0 (even slice) or 2 (odd slice) is
+// the byte of the half's own block.
 __device__ __forceinline__ void mx4_spread(uint32_t raw, uint32_t (&w)[2]) {
   const auto r = __builtin_amdgcn_permlane32_swap(raw, raw, false, false);
   const int sh = 8 * ((threadIdx.x & 63) >> 5);
@@ -1181,33 +1186,31 @@ __device__ __forceinline__ void mx4_spread(uint32_t raw, uint32_t (&w)[2]) {
   w[1] = (uint32_t)r[1] >> sh;
 }
 
-struct Mx4Src {
-  const bf16_t* A;
-  const bf16_t* W1;
-  const bf16_t* W3;
-  int KB, N;   // bytes of a row (K / 2), panel rows of an expert
-  template <bool FC1>
-  __device__ TileLoads loads(const Tile& t) const {
-    return tile_loads<FC1, false, 1>(t, A, W1, W3, KB, N, KB);
-  }
-};
+// Wait until at most n of this wave's vector-memory instructions are in flight; they end in
+// the order they were issued in.
+__device__ __forceinline__ void wait_vm(int n) {
+  if (n == 16) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+  else if (n == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+  else if (n == 4) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
 
-// The bf16 main loop's pipeline on 256-value steps (see mainloop and, for the scale words
-// that run one step ahead, mainloop_mx). nkw: 128-value words of a row.
+// The bf16 main loop's pipeline on 256-value steps (see mainloop). scl: LDS address of the
+// two stages' scale words; pend: stores of the tile before that may stay in flight past this
+// tile's first step (its loads are older).
 template <bool FC1, bool HALF, bool GUARD>
-__device__ __forceinline__ void mainloop_mx4(char* smem, const TileLoads& ld, int kb, int ke,
-                                             int stage0, bool primed, const Tile& nt,
-                                             const Mx4Src& src, bool has_next, int nkb,
-                                             const Tile& t, const MxScales& ms, int E, int nkw,
+__device__ __forceinline__ void mainloop_mx4(char* smem, const char* scales, const TileLoads& ld,
+                                             int kb, int ke, int stage0, bool primed, int pend,
+                                             const Tile& nt, const Mx4Src& src, bool has_next,
+                                             int nkb, const Tile& t,
                                              f32x16 (&acc)[HALF ? 2 : 4][2]) {
   constexpr int WM = HALF ? 2 : 4;
   constexpr int WN = 2;
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int arow0 = (wave & 1) * (HALF ? 64 : 128);
   const int prow0 = (wave >> 1) * 64;
-  const int fr = lane & 31;
-  const uint32_t lds0 = lds_addr(smem) + wave * 1024;
+  const uint32_t lds0 = lds_addr(smem) + wave * 1024, scl0 = lds_addr(scales);
   const int nmb = GUARD ? max(0, min(WM, (t.vrows - arow0 + 31) >> 5)) : WM;
 #pragma unroll
   for (int i = 0; i < WM; ++i)
@@ -1218,34 +1221,30 @@ __device__ __forceinline__ void mainloop_mx4(char* smem, const TileLoads& ld, in
   if (!primed) {
     issue_loads(ld, lds0 + stage0 * STAGE_BYTES, kb, 0);
     issue_loads(ld, lds0 + stage0 * STAGE_BYTES, kb, 1);
+    src.template issue_scales<FC1>(t, kb, scl0 + stage0 * MX4_SCALES);
+    pend = 0;
   }
-  uint32_t na[WM], nw[WN];
-  mx4_scale_words<FC1, HALF>(t, ms, E, src.N, nkw, kb, na, nw);
   auto step = [&](int kt, auto issue) {
     const int cur = (stage0 + kt - kb) & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    wait_vm(kt == kb ? pend : 0);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    // taken here, where every load has landed: a later use would make the compiler wait
-    // for these words behind the next stage's copies
-    uint32_t sa[WM][2], sw[WN][2];
-#pragma unroll
-    for (int i = 0; i < WM; ++i) {
-      mx4_spread(na[i], sa[i]);
-      asm volatile("" ::"v"(sa[i][0]), "v"(sa[i][1]));
-    }
-#pragma unroll
-    for (int i = 0; i < WN; ++i) {
-      mx4_spread(nw[i], sw[i]);
-      asm volatile("" ::"v"(sw[i][0]), "v"(sw[i][1]));
-    }
-    if (kt + 1 < ke) mx4_scale_words<FC1, HALF>(t, ms, E, src.N, nkw, kt + 1, na, nw);
     const char* sA = smem + cur * STAGE_BYTES;
     const char* sB = sA + A_BYTES;
-    const uint32_t lnext = lds0 + (cur ^ 1) * STAGE_BYTES;
+    // word `half` of the lane's rows
+    const char* sc = scales + cur * MX4_SCALES + half * 1024;
+    auto word = [&](int piece, int row) {
+      return *reinterpret_cast<const uint32_t*>(sc + piece * 2048 + row * 4);
+    };
+    uint32_t sa[WM][2], sw[WN][2];
+#pragma unroll
+    for (int mb = 0; mb < WM; ++mb) mx4_spread(word(0, arow0 + mb * 32 + fr), sa[mb]);
+#pragma unroll
+    for (int nb = 0; nb < WN; ++nb)
+      mx4_spread(FC1 ? word(1 + nb, prow0 / 2 + fr) : word(1, prow0 + 32 * nb + fr), sw[nb]);
     uint4 wf[2][WN], af[2][WM];
     auto frag = [&](int ks, int buf) {
-      const int chk = ks * 2 + (lane >> 5);
+      const int chk = ks * 2 + half;
 #pragma unroll
       for (int nb = 0; nb < WN; ++nb)
         wf[buf][nb] = *reinterpret_cast<const uint4*>(sB + swz(prow0 + nb * 32 + fr, chk));
@@ -1256,12 +1255,12 @@ __device__ __forceinline__ void mainloop_mx4(char* smem, const TileLoads& ld, in
     auto op = [](const uint4& v) {
       return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
     };
-    const bool two = 2 * kt + 1 >= nkw;   // the row's last word: two slices
+    const bool two = 2 * kt + 1 >= src.KB / 64;   // the row's last word: two slices
     frag(0, 0);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       if (ks == 2 && two) break;
-      if (ks < 2) issue(lnext, ks);
+      if (ks < 2) issue(cur ^ 1, ks);
       if (ks + 1 < 4) frag(ks + 1, (ks + 1) & 1);
 #pragma unroll
       for (int mb = 0; mb < WM; ++mb) {
@@ -1280,24 +1279,61 @@ __device__ __forceinline__ void mainloop_mx4(char* smem, const TileLoads& ld, in
   };
   int kt = kb;
   for (; kt + 1 < ke; ++kt)
-    step(kt, [&](uint32_t l, int ks) { issue_loads<HALF ? 2 : 4>(ld, l, kt + 1, ks); });
+    step(kt, [&](int st, int ks) {
+      issue_loads<HALF ? 2 : 4>(ld, lds0 + st * STAGE_BYTES, kt + 1, ks);
+      if (ks == 1) src.template issue_scales<FC1>(t, kt + 1, scl0 + st * MX4_SCALES);
+    });
   const TileLoads nxt = src.template loads<FC1>(nt);   // nt is this tile without a next one
-  step(kt, [&](uint32_t l, int ks) {
-    if (has_next) issue_loads(nxt, l, nkb, ks);
+  step(kt, [&](int st, int ks) {
+    if (!has_next) return;
+    issue_loads(nxt, lds0 + st * STAGE_BYTES, nkb, ks);
+    if (ks == 1) src.template issue_scales<FC1>(nt, nkb, scl0 + st * MX4_SCALES);
   });
 }
 
+// The tile's results from the accumulators: 16 columns of a row a lane, 32 bytes. Returns the
+// number of stores, the same for every lane.
+template <int MODE, bool HALF>
+__device__ __forceinline__ int mx4_epilogue(const Tile& t, const Epi& ep,
+                                            const f32x16 (&acc)[HALF ? 2 : 4][2]) {
+  constexpr int WM = HALF ? 2 : 4;
+  constexpr int WN = MODE == kFc1 ? 1 : 2;   // blocks of 32 output columns
+  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = ep.N, n0 = t.n0 + (wave >> 1) * (32 * WN);
+  if (n0 >= N) return 0;   // N is a multiple of 64
+  const rows_t rc = tile_rows(ep.C + (size_t)t.m0 * N, t.rows * N * 2);
+  const int oc = (fr * N + 16 * half) * 2;
+#pragma unroll
+  for (int mb = 0; mb < WM; ++mb) {
+    const int r = (wave & 1) * (HALF ? 64 : 128) + mb * 32;
+#pragma unroll
+    for (int nb = 0; nb < WN; ++nb) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = MODE == kFc1 ? silu_mul(acc[mb][0][i], acc[mb][1][i]) : acc[mb][nb][i];
+      run16_out(rc, oc + (r * N + n0 + 32 * nb) * 2, v);
+    }
+  }
+  return 2 * WM * WN;
+}
+
 template <int MODE, bool HALF, bool GUARD>
-__device__ __forceinline__ void run_tile_mx4(char* smem, const Tile& t, const Epi& ep, int kb,
-                                             int ke, float* __restrict__ part, int stage0,
-                                             bool primed, const Tile& nt, bool has_next, int nkb,
-                                             const Mx4Src& src, const MxScales& ms, int E,
-                                             int nkw) {
+__device__ __forceinline__ int run_tile_mx4(char* smem, const char* scales, const Tile& t,
+                                            const Epi& ep, int kb, int ke,
+                                            float* __restrict__ part, int stage0, bool primed,
+                                            int pend, const Tile& nt, bool has_next, int nkb,
+                                            const Mx4Src& src) {
   f32x16 acc[HALF ? 2 : 4][2];
   const TileLoads ld = src.template loads<MODE == kFc1>(t);
-  mainloop_mx4<MODE == kFc1, HALF, GUARD>(smem, ld, kb, ke, stage0, primed, nt, src, has_next,
-                                          nkb, t, ms, E, nkw, acc);
-  finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc);
+  mainloop_mx4<MODE == kFc1, HALF, GUARD>(smem, scales, ld, kb, ke, stage0, primed, pend, nt, src,
+                                          has_next, nkb, t, acc);
+  if (part) {
+    finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc);
+    return 0;
+  }
+  return mx4_epilogue<MODE, HALF>(t, ep, acc);
 }
 
 // The rows of each expert: contiguous segments [offsets[e], offsets[e+1]) (cap = 0), of
@@ -1548,6 +1584,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_mx4_kernel(const bf16_t* __restric
                                                          MxScales ms) {
   constexpr bool FC1 = is_fc1(MODE);
   __shared__ __attribute__((aligned(16))) char smem[2 * STAGE_BYTES];
+  __shared__ __attribute__((aligned(16))) char scales[2 * MX4_SCALES];
   __shared__ Sched sc;
   build_sched(sc, sg, E, m_cap);
 
@@ -1583,30 +1620,26 @@ __global__ __launch_bounds__(NTHR, 1) void gg_mx4_kernel(const bf16_t* __restric
   };
 
   if (vb >= items) return;
-  const Mx4Src src{A, W1, W3, KB, N};
-  const int nkw = KB / 64;
+  const Mx4Src src{A, W1, W3, ms, KB, N, E};
   Work cur = work(vb);
   int stage0 = 0;
   bool primed = false;
+  int pend = 0;
   for (int w = vb; w < items; w += gridDim.x) {
     const bool has_next = w + (int)gridDim.x < items;
     const Work nw = has_next ? work(w + gridDim.x) : cur;
     const bool guard = cur.t.vrows < cur.t.rows;
-    if (cur.t.rows > BM / 2) {
-      if (guard)
-        run_tile_mx4<MODE, false, true>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, stage0, primed,
-                                        nw.t, has_next, nw.kb, src, ms, E, nkw);
-      else
-        run_tile_mx4<MODE, false, false>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, stage0,
-                                         primed, nw.t, has_next, nw.kb, src, ms, E, nkw);
-    } else {
-      if (guard)
-        run_tile_mx4<MODE, true, true>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, stage0, primed,
-                                       nw.t, has_next, nw.kb, src, ms, E, nkw);
-      else
-        run_tile_mx4<MODE, true, false>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, stage0,
-                                        primed, nw.t, has_next, nw.kb, src, ms, E, nkw);
-    }
+    const auto run = [&](auto half, auto grd) {
+      return run_tile_mx4<MODE, decltype(half)::value, decltype(grd)::value>(
+          smem, scales, cur.t, ep, cur.kb, cur.ke, cur.part, stage0, primed, pend, nw.t, has_next,
+          nw.kb, src);
+    };
+    const std::true_type yes{};
+    const std::false_type no{};
+    if (cur.t.rows > BM / 2)
+      pend = guard ? run(no, yes) : run(no, no);
+    else
+      pend = guard ? run(yes, yes) : run(yes, no);
     stage0 = (stage0 + cur.ke - cur.kb) & 1;
     primed = has_next;
     cur = nw;

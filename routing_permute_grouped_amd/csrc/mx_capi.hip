@@ -91,8 +91,8 @@ moe_status_t moe_grouped_fc1_swiglu_mxfp4(const void* xq_perm, const void* xs_pe
                                           const void* w1s, const void* w3q, const void* w3s,
                                           void* h, void* workspace, size_t ws_bytes,
                                           void* stream) {
-  if (!aligned16(xq_perm) || !aligned4(xs_perm) || !aligned16(w1q) || !aligned4(w1s) ||
-      !aligned16(w3q) || !aligned4(w3s) || !aligned16(h))
+  if (!aligned16(xq_perm) || !aligned16(xs_perm) || !aligned16(w1q) || !aligned16(w1s) ||
+      !aligned16(w3q) || !aligned16(w3s) || !aligned16(h))
     return MOE_EINVAL;
   const moe_status_t st =
       segments_ok(offsets, counts, tile_expert, E, D, F, m_tile, m_cap, workspace);
@@ -109,7 +109,7 @@ moe_status_t moe_grouped_fc2_mxfp4(const void* hq, const void* hs, const int32_t
                                    int D, int F, int m_tile, int64_t m_cap, const void* w2q,
                                    const void* w2s, void* y_perm, void* workspace,
                                    size_t ws_bytes, void* stream) {
-  if (!aligned16(hq) || !aligned4(hs) || !aligned16(w2q) || !aligned4(w2s) || !aligned16(y_perm))
+  if (!aligned16(hq) || !aligned16(hs) || !aligned16(w2q) || !aligned16(w2s) || !aligned16(y_perm))
     return MOE_EINVAL;
   const moe_status_t st =
       segments_ok(offsets, counts, tile_expert, E, D, F, m_tile, m_cap, workspace);

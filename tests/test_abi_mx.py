@@ -76,7 +76,7 @@ def fc2(xq=FAKE, xs=FAKE, offs=FAKE, counts=None, te=FAKE, E=8, D=256, F=320, mt
 
 @pytest.mark.parametrize("call", [fc1, fc2])
 @pytest.mark.parametrize("kw,code", [
-    (dict(xq=None), MOE_EINVAL), (dict(xs=FAKE + 2), MOE_EINVAL), (dict(offs=None), MOE_EINVAL),
+    (dict(xq=None), MOE_EINVAL), (dict(xs=FAKE + 8), MOE_EINVAL), (dict(offs=None), MOE_EINVAL),
     (dict(counts=FAKE + 2), MOE_EINVAL), (dict(te=None), MOE_EINVAL),
     (dict(w1q=FAKE + 8), MOE_EINVAL), (dict(h=None), MOE_EINVAL),
     (dict(ws=FAKE + 8, wsb=1 << 20), MOE_EINVAL), (dict(E=0), MOE_ESHAPE),
