@@ -92,17 +92,20 @@ def moe_quantize_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     multiple of 32); MOE_MX_KSTEPS, the products' k-step words as uint8 [C/128, R, 4] (R
     rows, C a multiple of 128)."""
     B._layer_dtype(x, "x")
-    if x.dim() < 1 or x.numel() == 0:
+    n = x.numel()
+    if n == 0 or x.dim() < 1:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected rows of values")
-    C = x.shape[-1]
-    R = x.numel() // C
-    B._numel(q, "q", R * C // 2, torch.uint8)
-    B._numel(scales, "scales", _scale_bytes(R, C), torch.uint8)
+    *lead, C = x.shape
+    R = n // C
     if q is None:
-        q = torch.empty((*x.shape[:-1], C // 2), dtype=torch.uint8, device=x.device)
+        q = x.new_empty((*lead, C // 2), dtype=torch.uint8)
+    else:
+        B._numel(q, "q", n // 2, torch.uint8)
     if scales is None:
-        shape = (C // 128, R, 4) if layout == B.MOE_MX_KSTEPS else (*x.shape[:-1], C // 32)
-        scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        scales = x.new_empty((C // 128, R, 4) if layout == B.MOE_MX_KSTEPS else (*lead, C // 32),
+                             dtype=torch.uint8)
+    else:
+        B._numel(scales, "scales", _scale_bytes(R, C), torch.uint8)
     _run("moe_quantize_mxfp4", stream, B._dt(x), ("x", x), R, C, ("q", q), ("scales", scales),
          layout)
     return q, scales
@@ -114,9 +117,10 @@ def _dequantize(name: str, per: int, q, scales, out, layout, dtype, stream) -> t
     if out is None:
         if dtype not in B._LAYER_DTYPES:
             raise TypeError(f"dtype {dtype}, expected float32 or bfloat16")
-        out = torch.empty((*q.shape[:-1], C), dtype=dtype, device=q.device)
-    B._layer_dtype(out, "out")
-    B._numel(out, "out", R * C)
+        out = q.new_empty((*q.shape[:-1], C), dtype=dtype)
+    else:
+        B._layer_dtype(out, "out")
+        B._numel(out, "out", R * C)
     _run(name, stream, B._dt(out), ("q", q), ("scales", scales), R, C, layout, ("out", out))
     return out
 
