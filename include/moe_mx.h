@@ -100,8 +100,9 @@ moe_status_t moe_grouped_fc2_mxfp4(const void* hq, const void* hs, const int32_t
  *   h = silu(x w1[e]^T) * (x w3[e]^T) rounded to bf16, y = h w2[e]^T rounded to bf16,
  * float32 sums; the other rows of x_masked, h and y are neither read nor written, and an
  * expert without rows has none of its weights read. The weights' values enter the products
- * exactly (a 4-bit code times a power of two is a bf16 value). Each 128 rows of a slab read
- * the weights once.
+ * exactly (a 4-bit code times a power of two is a bf16 value). Each 64 rows of a slab read
+ * the weights once. Calls with few rows in all sum over k in two halves, so a row's last bits
+ * may depend on how many other rows there are; equal calls give equal bits.
  *   x_masked [E*cap,D], w1q, w3q [E,F,D/2], w2q [E,D,F/2], scales in MOE_MX_KSTEPS over the
  *   weights' rows -> h [E*cap,F], y [E*cap,D].
  * D and F multiples of 128, D*F < 2^31; cap a multiple of 16, at most 65536, E*cap < 2^31.

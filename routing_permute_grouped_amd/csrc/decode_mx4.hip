@@ -7,7 +7,8 @@
 // bf16 stream; per weight byte there is four times the work on the rows. Hence
 //   * a work item is 64 output columns for up to 64 rows of one expert; a workgroup of four
 //     waves takes one item after the other, each wave 16 of the columns: rows of w1 and of w3
-//     (fc1: one row fragment feeds both), or of w2;
+//     (fc1: one row fragment feeds both), or of w2. Where such items are too few for the CUs,
+//     an item is 32 columns, and two waves halve the k of 16;
 //   * a lane loads 16 bytes of a weight row: one whole MX block, so one scale serves them.
 //     Lane group g holds block g of a 128-value chunk, and its 8-code words are the four
 //     MFMA slices; the rows' fragments follow the same order (any order of k serves that
@@ -21,7 +22,7 @@
 //     are ordinary ones, so every wait is the compiler's own;
 //   * four workgroups a CU hide the latency; deeper prefetch at three or two was slower (64
 //     experts of D = 2048, F = 1408, one row each: 57 us, at two workgroups and 16 chunks
-//     ahead 94), and so was splitting k over the waves (100 us);
+//     ahead 94), and so was splitting k over all four waves (100 us);
 //   * the items that exist are found on the device from the counts, so that experts without
 //     rows and unused row groups cost no workgroup (one that looks up its count and leaves
 //     holds its place for more than a microsecond: 20 of 87 us with half of them empty).
@@ -35,7 +36,7 @@ namespace moe {
 namespace {
 
 constexpr int DW = 4;           // waves per workgroup
-constexpr int GROUP = 64;       // rows per workgroup
+constexpr int GROUP = 64;       // rows of an item
 constexpr int XBYTES = 32768;   // two row buffers: 16*NB rows of KS chunks (256 bytes) each
 constexpr int XCDS = 8;
 
@@ -101,42 +102,46 @@ __device__ __forceinline__ void spread(uint32_t word, int g, float (&scale)[KS])
 }
 
 // NB: row blocks of 16 of the item's rows; KS: 128-value chunks per LDS buffer; PD: groups of
-// KS weight chunks in flight. cols: the item's first column.
-template <bool FC1, int NB, int KS, int PD>
+// chunks in flight; KW: waves that share 16 columns, each taking every KW-th chunk (the item is
+// 64 / KW columns, and their sums are added in wave order). cols: the item's first column.
+template <bool FC1, int NB, int KS, int PD, int KW>
 __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X, int cols, int e,
                                           int r0, int rows, int K, int N, int E,
                                           const Mx4Weights& wt, bf16_t* __restrict__ out) {
   constexpr int NW = FC1 ? 2 : 1;                 // weight fragments a wave multiplies
   constexpr int ROWB = KS * 256;                  // bytes of a row's group of chunks
   constexpr int NX = NB * KS;                     // 16-byte units per thread and group
+  constexpr int KC = KS / KW;                     // chunks of a group a wave takes
   static_assert(2 * NB * 16 * ROWB <= XBYTES, "two row buffers");
   // opaque per item, so that addresses derived from it are not kept across the items: with
-  // four bodies in the item loop they would not fit the registers
+  // six bodies in the item loop they would not fit the registers
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 15, g = lane >> 4;
-  const int n0 = cols + wave * 16;
+  const int kw = KW > 1 ? wave / (DW / KW) : 0;
+  const int n0 = cols + wave % (DW / KW) * 16;
   const int nch = K / 128;
   const int ngr = (nch + KS - 1) / KS;
 
-  // this lane's weight rows, and their scale words of chunk g % KS of a group
+  // this lane's weight rows, and their scale words of the wave's chunk g % KC of a group
   const size_t row = (size_t)e * N + n0 + fr;
   const uint8_t* wrow[2] = {wt.q1 + row * (K / 2) + 16 * g, wt.q2 + row * (K / 2) + 16 * g};
   const uint32_t* srow[2] = {wt.s1 + row, wt.s2 + row};
   const size_t sstep = (size_t)E * N;
-  u32x4 wr[PD][NW][KS];
+  u32x4 wr[PD][NW][KC];
   uint32_t sr[PD][NW];
   // past the last chunk of a group that K ends in, the last one again; its rows are zeros there
   auto wload = [&](int slot, int gr) {
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      const int c = min(gr * KS + i, nch - 1);
+    for (int i = 0; i < KC; ++i) {
+      const int c = min(gr * KS + i * KW + kw, nch - 1);
 #pragma unroll
       for (int w = 0; w < NW; ++w) wr[slot][w][i] = ld16(wrow[w] + (size_t)c * 64);
     }
 #pragma unroll
-    for (int w = 0; w < NW; ++w) sr[slot][w] = srow[w][min(gr * KS + g % KS, nch - 1) * sstep];
+    for (int w = 0; w < NW; ++w)
+      sr[slot][w] = srow[w][min(gr * KS + g % KC * KW + kw, nch - 1) * sstep];
   };
 
   // unit q of a group: row q / (16*KS), 16-byte unit q % (16*KS) of the row's group
@@ -169,11 +174,11 @@ __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X
 
   auto compute = [&](int buf, int slot) {
     const char* xb = xs + buf * (XBYTES / 2);
-    float scale[NW][KS];
+    float scale[NW][KC];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) spread<KS>(sr[slot][w], g, scale[w]);
+    for (int w = 0; w < NW; ++w) spread<KC>(sr[slot][w], g, scale[w]);
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
+    for (int i = 0; i < KC; ++i) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         bf16x8 wf[NW];
@@ -183,7 +188,7 @@ __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X
         for (int b = 0; b < NB; ++b) {
           const int r = 16 * b + fr;
           const bf16x8 xf = __builtin_bit_cast(
-              bf16x8, ld16(xb + r * ROWB + i * 256 + (((4 * g + s) ^ (r & 15)) << 4)));
+              bf16x8, ld16(xb + r * ROWB + (i * KW + kw) * 256 + (((4 * g + s) ^ (r & 15)) << 4)));
 #pragma unroll
           for (int w = 0; w < NW; ++w)
             acc[w][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[w], xf, acc[w][b], 0, 0, 0);
@@ -215,6 +220,25 @@ __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X
     }
   }
 
+  if (KW > 1) {   // every wave is past its last read of the row buffers
+    f32x4* red = reinterpret_cast<f32x4*>(xs) + wave % (DW / KW) * ((KW - 1) * NW * NB * 64) + lane;
+    if (kw > 0) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) red[(((kw - 1) * NW + w) * NB + b) * 64] = acc[w][b];
+    }
+    lds_barrier();
+    if (kw == 0) {
+#pragma unroll
+      for (int o = 0; o < KW - 1; ++o)
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[w][b] += red[((o * NW + w) * NB + b) * 64];
+    }
+    if (kw > 0) return;   // from this item; the next one begins with a barrier
+  }
   // lane l holds row 16*b + l%16 and output columns 4*(l/16) .. +3 of its 16
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -263,14 +287,24 @@ template <bool FC1>
 __global__ __launch_bounds__(DW * 64, 4) void dec4_kernel(const bf16_t* __restrict__ X,
                                                           const int32_t* __restrict__ counts,
                                                           int cap, int E, int K, int N,
-                                                          Mx4Weights wt,
+                                                          int cus, Mx4Weights wt,
                                                           bf16_t* __restrict__ out) {
   __shared__ __attribute__((aligned(1024))) char xs[XBYTES];
   const int lane = threadIdx.x & 63;
-  const int per = (E + 63) / 64, ncols = N / 64;
+  const int per = (E + 63) / 64;
   int sum = 0, groups;
-  for (int i = 0; i < per; ++i) sum += row_groups(counts, lane * per + i, E, cap);
+  bool tall = false;   // an expert with more than 32 rows
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    sum += row_groups(counts, e, E, cap);
+    tall |= e < E && min(counts[e], cap) > 32;
+  }
   const int start = wave_scan(sum, groups);
+  // with at most one 64-column item a CU, two waves share 16 columns: twice the items, half
+  // the chain of loads (one token over 6 of 64 experts 17.9 -> 15.9 us; at two items a CU, K =
+  // 14336, 158 -> 179 us). Two LDS chunks of more than 32 rows would not fit.
+  const bool halve = groups * (N / 64) <= cus && __ballot(tall) == 0;
+  const int width0 = halve ? 32 : 64, ncols = N / width0;
   const int items = groups * ncols;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int grp = item / ncols;
@@ -287,26 +321,30 @@ __global__ __launch_bounds__(DW * 64, 4) void dec4_kernel(const bf16_t* __restri
     const int local = item - s * ncols;
     const int base = local / (XCDS * ng) * XCDS, in = local - base * ng;
     const int width = min(XCDS, ncols - base);
-    const int first = in / width * GROUP, cols = (base + in % width) * 64;
+    const int first = in / width * GROUP, cols = (base + in % width) * width0;
     const int rows = min(n - first, GROUP), r0 = e * cap + first;
-    if (rows <= 16)
-      dec4_body<FC1, 1, 4, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+    if (rows <= 16 && halve)
+      dec4_body<FC1, 1, 4, 1, 2>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+    else if (rows <= 16)
+      dec4_body<FC1, 1, 4, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+    else if (rows <= 32 && halve)
+      dec4_body<FC1, 2, 2, 1, 2>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
     else if (rows <= 32)
-      dec4_body<FC1, 2, 2, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 2, 2, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
     else if (rows <= 48)
-      dec4_body<FC1, 3, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 3, 1, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
     else
-      dec4_body<FC1, 4, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 4, 1, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
   }
 }
 
 template <bool FC1>
 void launch_dec4(const void* X, const int32_t* counts, int cap, int E, int K, int N,
                  const Mx4Weights& wt, void* out, hipStream_t s) {
-  const int64_t most = (int64_t)E * ((cap + GROUP - 1) / GROUP) * (N / 64);
+  const int64_t most = (int64_t)E * ((cap + GROUP - 1) / GROUP) * (N / 32);
   const int grid = (int)std::min<int64_t>(4 * cu_count(), most);
   hipLaunchKernelGGL(dec4_kernel<FC1>, dim3(grid), dim3(DW * 64), 0, s,
-                     static_cast<const bf16_t*>(X), counts, cap, E, K, N, wt,
+                     static_cast<const bf16_t*>(X), counts, cap, E, K, N, cu_count(), wt,
                      static_cast<bf16_t*>(out));
 }
 

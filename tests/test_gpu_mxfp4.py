@@ -304,6 +304,10 @@ DECODE = {   # counts, cap, D, F
     "more_than_the_slab": ([40, -3, 100], 16, 128, 128),
     "many_experts": ([2, 0, 1] * 40, 16, 128, 256),
     "odd_chunks": ([7], 16, 1152, 1408),
+    # more items of 64 columns than the card has compute units
+    "many_items": ([3, 0, 20, 16, 32, 1] * 11, 32, 384, 512),
+    "many_items_tall": ([16, 40, 17, 64, 0, 33] * 11, 64, 384, 512),
+    "most_experts": ([0] * 511 + [5, 0, 17] + [1, 0, 0] * 170, 32, 128, 128),
 }
 
 
