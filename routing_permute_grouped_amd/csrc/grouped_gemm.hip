@@ -1352,9 +1352,11 @@ struct Sched {
   int segoff[MAXE + 1];   // segment starts (clamped to the rows in use)
   int segend[MAXE];       // segment ends
   int segval[MAXE];       // ends of the rows that hold tokens (segoff <= segval <= segend)
-  int tstart[MAXE + 1];   // first 256-row block of each expert
+  int tstart[MAXE + 1];   // first row block of each expert
   int wtot[16];
 };
+
+__device__ void sched_blocks(Sched& sc, int E, int bm);
 
 __device__ void build_sched(Sched& sc, const Segs& sg, int E, int m_cap) {
   const int tid = threadIdx.x;
@@ -1379,12 +1381,18 @@ __device__ void build_sched(Sched& sc, const Segs& sg, int E, int m_cap) {
     }
   }
   __syncthreads();
+  sched_blocks(sc, E, BM);
+}
+
+// Row blocks of bm rows.
+__device__ void sched_blocks(Sched& sc, int E, int bm) {
+  const int tid = threadIdx.x;
   const int per = (MAXE + blockDim.x - 1) / blockDim.x;   // experts per thread (<= 4)
   int cnt[4], local = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = tid * per + i;
-    cnt[i] = (i < per && e < E) ? (max(sc.segend[e] - sc.segoff[e], 0) + BM - 1) / BM : 0;
+    cnt[i] = (i < per && e < E) ? (max(sc.segend[e] - sc.segoff[e], 0) + bm - 1) / bm : 0;
     local += cnt[i];
   }
   int run = block_scan_excl(local, sc.wtot);
@@ -1402,7 +1410,7 @@ __device__ void build_sched(Sched& sc, const Segs& sg, int E, int m_cap) {
 // nb_e row blocks x n_nt column tiles, walked in groups of up to GROUP_M row blocks per
 // column sweep so every weight panel is used by all (or GROUP_M) row blocks of its
 // expert back to back.
-__device__ Tile decode_item(const Sched& sc, int E, int n_nt, int cols, int w) {
+__device__ Tile decode_item(const Sched& sc, int E, int n_nt, int cols, int w, int bm = BM) {
   const int blk = w / n_nt;
   int lo = 0, hi = E;   // largest expert whose first block is <= blk
   while (hi - lo > 1) {
@@ -1419,8 +1427,8 @@ __device__ Tile decode_item(const Sched& sc, int E, int n_nt, int cols, int w) {
   const int mb = sc.tstart[lo] + first + within % gm;
   Tile t;
   t.e = lo;
-  t.m0 = sc.segoff[lo] + (mb - sc.tstart[lo]) * BM;
-  t.rows = min(BM, sc.segend[lo] - t.m0);
+  t.m0 = sc.segoff[lo] + (mb - sc.tstart[lo]) * bm;
+  t.rows = min(bm, sc.segend[lo] - t.m0);
   t.vrows = max(0, min(t.rows, sc.segval[lo] - t.m0));
   t.n0 = (within / gm) * cols;
   return t;
@@ -1433,12 +1441,12 @@ __device__ Tile decode_item(const Sched& sc, int E, int n_nt, int cols, int w) {
 // order sh = 0..S-1. Items [0, full) are whole tiles.
 //
 // min_saved: a tile is cut only if that saves at least so many k-steps of the round. The
-// 4-bit products and the checkpoint's two GEMMs ask for 12: writing, reading and adding
-// the shares costs 7 to 15 us, about 10 steps. (Measured with and without the split: fc1
-// on the checkpoint, 389 tokens top-2, D = 512 (5 steps saved) 32.9 against 25.6 us, D =
-// 1024 (10) 33.1 against 27.9, D = 2048 (21) 38.4 against 43.1; 4-bit fc2, 512 tokens top-2,
-// F = 2048 (5) 29.4 against 19.2 us, F = 8192 (21) 35.6 against 57.8.)
-constexpr int kMinSaved = 12;
+// 4-bit products and the checkpoint's two GEMMs ask for 20: writing, reading and adding the
+// shares costs 7 to 15 us, and a reduction that finds nothing to add 4. (Cut against uncut in
+// halved row blocks, 200 tokens of one expert, 2048 columns: fc1 with the checkpoint, D = 1024
+// (14 steps saved) 36.3 against 25.9 us, D = 2048 (28) 36.2 against 37.1; 4-bit fc2, F = 4096
+// (14) 27.4 against 25.3 us, F = 8192 (28) 30.4 against 40.6.)
+constexpr int kMinSaved = 20;
 
 struct Split {
   int full, tail, S, nks;
@@ -1471,6 +1479,33 @@ __device__ Split split_plan(int total, int G, int slots, int nk, int min_saved) 
   return p;
 }
 
+// The 4-bit products and the checkpoint's two GEMMs halve the row blocks where whole tiles
+// would leave half of the workgroups idle, unless a cut over k puts at least three of them on
+// a tile. (Halves against whole tiles, 1500 tokens top-2 over 8 experts, F = 1024: fc1 with the
+// checkpoint, D = 1024 29.9 against 39.0 us; its backward, D = 512 29.8 against 39.7; 4-bit
+// fc1, D = 4096 28.0 against 36.7. Halves against a cut in two: 4-bit fc1, D = 8192 46.1 against
+// 57.1 us; against a cut in four: the backward, D = 2048 51.4 against 50.7, D = 4096 80.3 against
+// 62.9.)
+__device__ __forceinline__ bool may_halve(const Split& sp, int total, int G) {
+  return 2 * total <= G && sp.S <= 2;
+}
+
+// Whether an expert has more rows than half a block; without one the halves change nothing.
+__device__ bool tall_rows(const Sched& sc, int E) {
+  bool tall = false;
+  for (int e = threadIdx.x; e < E; e += blockDim.x)
+    tall |= sc.segend[e] - sc.segoff[e] > BM / 2;
+  return __syncthreads_or(tall) != 0;
+}
+
+// The block height for the plan sp of `total` tiles, and the plan and the tiles of that height.
+__device__ __forceinline__ int plan_rows(Sched& sc, int E, int n_nt, int total, int nk, Split& sp) {
+  if (!may_halve(sp, total, gridDim.x) || !tall_rows(sc, E)) return BM;
+  sched_blocks(sc, E, BM / 2);
+  sp = Split{sc.tstart[E] * n_nt, 0, 1, nk};
+  return BM / 2;
+}
+
 // P_MN: the weights are read MN-major (see tile_loads); ksplit as there. MX: fc1 on the
 // FP8 payload (A, W1, W3 hold e4m3 bytes, ms their scales).
 template <int MODE, bool P_MN, bool MX = false>
@@ -1488,7 +1523,8 @@ __global__ __launch_bounds__(NTHR, 1) void gg_bf16_kernel(
   const int n_nt = (N + cols - 1) / cols;
   const int total = sc.tstart[E] * n_nt;
   const int nk = K * EB / (BK * 2);   // 128-byte k-steps
-  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE));
+  Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE));
+  const int bm = MODE >= kFc1Q ? plan_rows(sc, E, n_nt, total, nk, sp) : BM;
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
   if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
@@ -1512,7 +1548,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_bf16_kernel(
       r.ke = min(nk, r.kb + sp.nks);
       r.part = ws + (size_t)j * (BM * BP);
     }
-    r.t = decode_item(sc, E, n_nt, cols, tile);
+    r.t = decode_item(sc, E, n_nt, cols, tile, bm);
     return r;
   };
 
@@ -1592,7 +1628,8 @@ __global__ __launch_bounds__(NTHR, 1) void gg_mx4_kernel(const bf16_t* __restric
   const int n_nt = (N + cols - 1) / cols;
   const int total = sc.tstart[E] * n_nt;
   const int nk = (KB + 127) / 128;
-  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, kMinSaved);
+  Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, kMinSaved);
+  const int bm = plan_rows(sc, E, n_nt, total, nk, sp);
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
   if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
@@ -1615,7 +1652,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_mx4_kernel(const bf16_t* __restric
       r.ke = min(nk, r.kb + sp.nks);
       r.part = ws + (size_t)j * (BM * BP);
     }
-    r.t = decode_item(sc, E, n_nt, cols, tile);
+    r.t = decode_item(sc, E, n_nt, cols, tile, bm);
     return r;
   };
 
@@ -1663,6 +1700,8 @@ struct SchedR {
   int off, end, val, ts;   // segment start and end, end of its token rows, first block
 };
 
+__device__ __forceinline__ void sched_blocks_r(SchedR& s, int bm, int& total);
+
 __device__ __forceinline__ SchedR build_sched_r(const Segs& sg, int E, int m_cap, int& total) {
   const int e = threadIdx.x & 63;
   SchedR s{0, 0, 0, 0};
@@ -1678,7 +1717,13 @@ __device__ __forceinline__ SchedR build_sched_r(const Segs& sg, int E, int m_cap
       s.val = sg.counts ? max(s.off, min(s.off + max(sg.counts[e], 0), s.end)) : s.end;
     }
   }
-  const int nb = (max(s.end - s.off, 0) + BM - 1) / BM;
+  sched_blocks_r(s, BM, total);
+  return s;
+}
+
+__device__ __forceinline__ void sched_blocks_r(SchedR& s, int bm, int& total) {
+  const int e = threadIdx.x & 63;
+  const int nb = (max(s.end - s.off, 0) + bm - 1) / bm;
   int inc = nb;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -1687,10 +1732,10 @@ __device__ __forceinline__ SchedR build_sched_r(const Segs& sg, int E, int m_cap
   }
   s.ts = inc - nb;
   total = __builtin_amdgcn_readlane(inc, 63);
-  return s;
 }
 
-__device__ __forceinline__ Tile decode_item_r(const SchedR& s, int E, int n_nt, int cols, int w) {
+__device__ __forceinline__ Tile decode_item_r(const SchedR& s, int E, int n_nt, int cols, int w,
+                                              int bm = BM) {
   const int lane = threadIdx.x & 63;
   const int blk = w / n_nt;
   const unsigned long long m = __ballot(lane < E && s.ts <= blk);
@@ -1699,7 +1744,7 @@ __device__ __forceinline__ Tile decode_item_r(const SchedR& s, int E, int n_nt, 
   const int off = __builtin_amdgcn_readlane(s.off, lo);
   const int end = __builtin_amdgcn_readlane(s.end, lo);
   const int val = __builtin_amdgcn_readlane(s.val, lo);
-  const int nb_e = (max(end - off, 0) + BM - 1) / BM;
+  const int nb_e = (max(end - off, 0) + bm - 1) / bm;
   const int local = w - ts * n_nt;
   const int gsz = min(GROUP_M, nb_e);
   const int grp = local / (gsz * n_nt);
@@ -1708,8 +1753,8 @@ __device__ __forceinline__ Tile decode_item_r(const SchedR& s, int E, int n_nt, 
   const int within = local - grp * gsz * n_nt;
   Tile t;
   t.e = lo;
-  t.m0 = off + (first + within % gm) * BM;
-  t.rows = min(BM, end - t.m0);
+  t.m0 = off + (first + within % gm) * bm;
+  t.rows = min(bm, end - t.m0);
   t.vrows = max(0, min(t.rows, val - t.m0));
   t.n0 = (within / gm) * cols;
   return t;
@@ -1815,13 +1860,20 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
   constexpr bool FC1 = is_fc1(MODE);
   __shared__ __attribute__((aligned(16))) char smem[RING_BYTES];
   int nblk;
-  const SchedR sr = build_sched_r(sg, E, m_cap, nblk);
+  SchedR sr = build_sched_r(sg, E, m_cap, nblk);
 
   const int cols = FC1 ? BP / 2 : BP;
   const int n_nt = (N + cols - 1) / cols;
   const int total = nblk * n_nt;
   const int nk = K / BK;
-  const Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE));
+  Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE));
+  int bm = BM;   // as plan_rows
+  if (MODE >= kFc1Q && may_halve(sp, total, gridDim.x) &&
+      __ballot(sr.end - sr.off > BM / 2) != 0) {
+    bm = BM / 2;
+    sched_blocks_r(sr, bm, nblk);
+    sp = Split{nblk * n_nt, 0, 1, nk};
+  }
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
   if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
@@ -1844,7 +1896,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
       r.ke = min(nk, r.kb + sp.nks);
       r.part = ws + (size_t)j * (BM * BP);
     }
-    r.t = decode_item_r(sr, E, n_nt, cols, tile);
+    r.t = decode_item_r(sr, E, n_nt, cols, tile, bm);
     return r;
   };
 
@@ -1902,8 +1954,10 @@ __global__ __launch_bounds__(256) void gg_tail_reduce(Segs sg, int E, int K, int
   const int N = ep.N;
   const int cols = FC1 ? BP / 2 : BP;
   const int n_nt = (N + cols - 1) / cols;
-  const Split sp = split_plan(sc.tstart[E] * n_nt, G, slots, K / BK, min_saved);
+  const int total = sc.tstart[E] * n_nt;
+  const Split sp = split_plan(total, G, slots, K / BK, min_saved);
   if (sp.tail == 0) return;
+  if (min_saved > 0 && may_halve(sp, total, G) && tall_rows(sc, E)) return;   // as plan_rows
   constexpr int Q = (FC1 ? BP / 2 : BP) / 4;   // 4-column groups per row
   const int64_t units = (int64_t)sp.tail * BM * Q;
   for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units;

@@ -51,6 +51,9 @@ SHAPES = {   # counts, mt, D, F
     "tall": ([1600], 256, 128, 192),                          # past the ring's row blocks
     "long_k_few_tiles": ([200, 60], 64, 4096, 256),           # the split last round
     "odd_mt32": ([40, 0, 130, 7] * 4, 32, 320, 448),
+    "whole_row_blocks": ([300, 257] * 7 + [256, 129], 64, 192, 1088),   # tiles for half the card
+    "cut_in_two": ([100] * 8, 64, 2560, 1408),                # the backward: in six
+    "halves_for_a_cut_in_two": ([2000], 64, 2560, 1408),      # the backward: cut in five
 }
 
 

@@ -197,7 +197,10 @@ SHAPES = {   # counts, mt, K, N
     "half_and_full_tiles": ([300, 128, 1, 256, 0, 257], 128, 640, 320),
     "fine": ([40, 0, 130, 7] * 16, 32, 256, 128),
     "many_experts": ([3, 0] * 100, 16, 128, 64),
-    "long_k_few_tiles": ([200, 60], 64, 4224, 256),       # the split last round, odd words
+    "long_k_few_tiles": ([200, 60], 64, 4224, 256),       # odd words, halved row blocks
+    "longer_k_few_tiles": ([200, 60], 64, 6528, 256),     # the split last round, odd words
+    "whole_row_blocks": ([300, 257] * 7 + [256, 129], 64, 384, 1088),   # tiles for half the card
+    "halves_for_a_cut_in_two": ([2000], 64, 10240, 1408), # fc2: cut in five
     "tall": ([1500], 256, 256, 576),
 }
 
