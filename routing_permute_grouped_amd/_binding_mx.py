@@ -379,6 +379,8 @@ def moe_grouped_dgrad_swiglu_ckpt8(dout_perm: torch.Tensor, offsets: torch.Tenso
             dtopk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
         if scratch is None:
             scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+            if stream is not None:   # freed on return, but that stream still uses it
+                scratch.record_stream(torch.cuda.ExternalStream(B._stream(stream), device=dev))
     _run("moe_grouped_dgrad_swiglu_ckpt8", stream, ("dout_perm", dout_perm), ("offsets", offsets),
          ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w2", w2),
          ("ab_codes", ab_codes), ("ab_scales", ab_scales), ("src_row", src_row),
