@@ -830,6 +830,22 @@ __device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep, co
   }
 }
 
+// Pad rows' sums to zero: their zero rows against an infinite or NaN weight would give NaN.
+template <bool HALF>
+__device__ __forceinline__ void zero_pads(const Tile& t, f32x16 (&acc)[HALF ? 2 : 4][2]) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int mb = 0; mb < (HALF ? 2 : 4); ++mb) {
+    const int r = (wave & 1) * (HALF ? 64 : 128) + 32 * mb;
+    if (r + 32 <= t.vrows) continue;
+    const bool pad = r + (int)(threadIdx.x & 31) >= t.vrows;
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[mb][nb][v] = pad ? 0.0f : acc[mb][nb][v];
+  }
+}
+
 // The end of a tile: the raw float32 sums of a split-K share (`part`, row-major
 // [BM][BP]) or the MODE epilogue. Lane l holds column m = l % 32 of every 32x32 block
 // and panel rows 8*g + 4*(l / 32) + i (i = 0..3) for g = 0..3.
@@ -925,6 +941,7 @@ __device__ __forceinline__ void run_tile(char* smem, const Tile& t, const TileLo
   if (MODE == kDgradQ) slots = wave_slots<HALF>(t, ep);
   mainloop<HALF, false, P_MN, GUARD>(smem, ld, kb, ke, stage0, primed, nxt, has_next, nkb, acc,
                                      t.vrows);
+  if (MODE >= kFc1Q && GUARD) zero_pads<HALF>(t, acc);
   finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc, nullptr, nullptr, slots);
 }
 
@@ -1329,6 +1346,7 @@ __device__ __forceinline__ int run_tile_mx4(char* smem, const char* scales, cons
   const TileLoads ld = src.template loads<MODE == kFc1>(t);
   mainloop_mx4<MODE == kFc1, HALF, GUARD>(smem, scales, ld, kb, ke, stage0, primed, pend, nt, src,
                                           has_next, nkb, t, acc);
+  if (GUARD) zero_pads<HALF>(t, acc);
   if (part) {
     finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc);
     return 0;
@@ -1925,11 +1943,13 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
       f32x16 acc[4][2];
       nbp = mainloop_ring<false>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
                                  nn, acc);
+      if (MODE == kFc1Q && cur.t.vrows < cur.t.rows) zero_pads<false>(cur.t, acc);
       finish_tile<MODE, false>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, 0, acc, elo, ehi);
     } else {
       f32x16 acc[2][2];
       nbp = mainloop_ring<true>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
                                 nn, acc);
+      if (MODE == kFc1Q && cur.t.vrows < cur.t.rows) zero_pads<true>(cur.t, acc);
       finish_tile<MODE, true>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, 0, acc, elo, ehi);
     }
     const int n = cur.ke - cur.kb;

@@ -230,6 +230,27 @@ def test_pad_rows_of_the_checkpoint_are_not_read(split):
         np.testing.assert_array_equal(a.view(np.uint8), b.view(np.uint8))
 
 
+@pytest.mark.parametrize("name", ["half_and_full_tiles", "many_experts", "long_k_few_tiles"])
+def test_pad_rows_are_zeros_beside_infinite_weights(name):
+    counts, mt, D, F = SHAPES[name]
+    c = use_case(counts, mt, D, F)
+    w = orc.values64(c["w2"]).copy()
+    w[:, 0, 0] = np.inf
+    c["w2"] = bf16(w)
+    dab, hw, _ = run_use(c, True)
+    pad = ~c["tok"]
+    pad[int(c["offs"][-1]):] = False
+    assert not orc.values64(dab[pad]).any() and not orc.values64(hw[pad]).any()
+    wt = P.to_dev(bf16(np.ascontiguousarray(w.transpose(0, 2, 1))))   # [E, F, D]
+    x, _ = token_rows(np.random.default_rng(7), counts, c["offs"], c["m_cap"], D)
+    h, q, s = rpg.moe_grouped_fc1_swiglu_ckpt8(
+        P.to_dev(x), P.to_dev(c["offs"]), P.to_dev(c["te"]), wt, wt, mt, c["m_cap"],
+        workspace=rpg.grouped_workspace("cuda"), counts=P.to_dev(np.array(counts, dtype=np.int32)))
+    torch.cuda.synchronize()
+    assert not orc.values64(P.to_host(h))[pad].any()
+    assert not P.to_host(q)[pad].any() and not P.to_host(s)[pad].any()
+
+
 def test_runs_repeat_bit_for_bit():
     c = use_case(*SHAPES["long_k_few_tiles"])
     first = run_use(c, True)
@@ -318,6 +339,26 @@ def test_weight_gradient_against_differences():
             u = d64[t] @ orc.values64(inp["w2"][e])
             bound = tol[t] + 2 * np.sqrt(((2.0 ** -3 * u * h) ** 2).sum())
             assert abs(float(diff[t]) - float(g["dtopk_w"][t, j])) <= bound
+
+
+def test_scratch_of_a_call_on_another_stream_is_its_own():
+    # the call's own scratch must not come back to this stream's allocator while it is in use
+    c = use_case(*SHAPES["many_experts"])
+    _, _, ref = run_use(c, False)
+    args = [P.to_dev(c[n]) for n in ("d", "offs", "te", "w2", "q", "s")]
+    kw = dict(src_row=P.to_dev(c["src"]), dst_row=P.to_dev(c["dst"]), topk_w=P.to_dev(c["w"]),
+              counts=P.to_dev(np.array(c["counts"], dtype=np.int32)))
+    n = rpg.moe_ckpt8_scratch_bytes(c["F"], c["m_cap"])
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        out = rpg.moe_grouped_dgrad_swiglu_ckpt8(*args, c["mt"], c["m_cap"], stream=stream, **kw)
+        mine = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all((m == 0x5A).all() for m in mine)
+        np.testing.assert_array_equal(P.to_host(out[2]), ref)
 
 
 def test_backward_on_streams_and_in_a_graph():

@@ -294,6 +294,23 @@ def test_a_nan_block_stays_in_its_row_and_its_column():
     assert not nan.any()
 
 
+@pytest.mark.parametrize("fc,K", [(1, 384), (2, 384), (1, 6528), (2, 6528)])
+def test_pad_rows_are_zeros_beside_a_nan_block(fc, K):
+    counts, mt, N = [20, 150, 1], 64, 128
+    rng = np.random.default_rng(4)
+    offs, te, m_cap = segments(counts, mt)
+    q, s, tok = rows4(rng, counts, offs, m_cap, K)
+    wq, wsc = mx.quantize_weights(bf16(rng.standard_normal((3, N, K))))
+    wsc[:, 70, 0] = 255
+    w = (P.to_dev(wq), P.to_dev(mx.words_of(wsc.reshape(3 * N, -1)))) * (3 - fc)
+    call = rpg.moe_grouped_fc1_swiglu_mxfp4 if fc == 1 else rpg.moe_grouped_fc2_mxfp4
+    y = call(P.to_dev(q), P.to_dev(mx.words_of(s)), P.to_dev(offs), P.to_dev(te), *w, mt,
+             workspace=rpg.grouped_workspace("cuda"), counts=P.to_dev(np.array(counts, dtype=np.int32)))
+    torch.cuda.synchronize()
+    y = orc.values64(P.to_host(y))
+    assert np.isnan(y[tok][:, 70]).all() and not y[~tok].any()
+
+
 # ---- decode ---------------------------------------------------------------------------
 
 DECODE = {   # counts, cap, D, F
