@@ -1181,15 +1181,24 @@ struct Mx4Src {
   // step, of the rows of A (w / 2 = 0), of the panel's w1 (or w2) rows (1), of its w3 rows (2).
   // Rows past the token rows get zero words (their codes are zeros, and a zero word cannot
   // turn those into NaN), and so does a word past the row's last.
+  struct Words {   // the wave's piece: its word 0 of the row block, its rows and bytes per word
+    const uint32_t* p;
+    int rows;
+    size_t step;
+  };
   template <bool FC1>
-  __device__ void issue_scales(const Tile& t, int kt, uint32_t lds) const {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int kind = wave >> 1, s = 2 * kt + (wave & 1);
-    if (kind >= (FC1 ? 3 : 2)) return;
-    const uint32_t* p = kind == 0 ? ms.a + (size_t)s * ms.ra + t.m0
-                                  : (kind == 1 ? ms.w1 : ms.w3) + ((size_t)s * E + t.e) * N + t.n0;
-    const int rows = s < KB / 64 ? (kind == 0 ? t.vrows : min(N - t.n0, BP)) : 0;
-    dma16(buffer_rsrc(p, (uint32_t)rows * 4u), (threadIdx.x & 63) * 16, 0, lds + wave * 1024);
+  __device__ Words words(const Tile& t) const {
+    const int kind = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >> 1;
+    if (kind == 0) return Words{ms.a + t.m0, t.vrows, (size_t)ms.ra};
+    const uint32_t* w = kind == 1 ? ms.w1 : ms.w3;
+    return Words{w + (size_t)t.e * N + t.n0, kind < (FC1 ? 3 : 2) ? min(N - t.n0, BP) : -1,
+                 (size_t)E * N};
+  }
+  __device__ void issue_words(const Words& w, int kt, uint32_t lds) const {
+    if (w.rows < 0) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), s = 2 * kt + (wave & 1);
+    dma16(buffer_rsrc(w.p + s * w.step, (uint32_t)(s < KB / 64 ? w.rows : 0) * 4u),
+          (threadIdx.x & 63) * 16, 0, lds + wave * 1024);
   }
 };
 
@@ -1228,6 +1237,7 @@ __device__ __forceinline__ void mainloop_mx4(char* smem, const char* scales, con
   const int arow0 = (wave & 1) * (HALF ? 64 : 128);
   const int prow0 = (wave >> 1) * 64;
   const uint32_t lds0 = lds_addr(smem) + wave * 1024, scl0 = lds_addr(scales);
+  const Mx4Src::Words words = src.template words<FC1>(t);
   const int nmb = GUARD ? max(0, min(WM, (t.vrows - arow0 + 31) >> 5)) : WM;
 #pragma unroll
   for (int i = 0; i < WM; ++i)
@@ -1238,12 +1248,11 @@ __device__ __forceinline__ void mainloop_mx4(char* smem, const char* scales, con
   if (!primed) {
     issue_loads(ld, lds0 + stage0 * STAGE_BYTES, kb, 0);
     issue_loads(ld, lds0 + stage0 * STAGE_BYTES, kb, 1);
-    src.template issue_scales<FC1>(t, kb, scl0 + stage0 * MX4_SCALES);
+    src.issue_words(words, kb, scl0 + stage0 * MX4_SCALES);
     pend = 0;
   }
-  auto step = [&](int kt, auto issue) {
+  auto step = [&](int kt, auto last, auto issue) {
     const int cur = (stage0 + kt - kb) & 1;
-    wait_vm(kt == kb ? pend : 0);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     const char* sA = smem + cur * STAGE_BYTES;
@@ -1254,11 +1263,6 @@ __device__ __forceinline__ void mainloop_mx4(char* smem, const char* scales, con
       return *reinterpret_cast<const uint32_t*>(sc + piece * 2048 + row * 4);
     };
     uint32_t sa[WM][2], sw[WN][2];
-#pragma unroll
-    for (int mb = 0; mb < WM; ++mb) mx4_spread(word(0, arow0 + mb * 32 + fr), sa[mb]);
-#pragma unroll
-    for (int nb = 0; nb < WN; ++nb)
-      mx4_spread(FC1 ? word(1 + nb, prow0 / 2 + fr) : word(1, prow0 + 32 * nb + fr), sw[nb]);
     uint4 wf[2][WN], af[2][WM];
     auto frag = [&](int ks, int buf) {
       const int chk = ks * 2 + half;
@@ -1272,13 +1276,24 @@ __device__ __forceinline__ void mainloop_mx4(char* smem, const char* scales, con
     auto op = [](const uint4& v) {
       return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
     };
-    const bool two = 2 * kt + 1 >= src.KB / 64;   // the row's last word: two slices
+#pragma unroll
+    for (int mb = 0; mb < WM; ++mb) sa[mb][0] = word(0, arow0 + mb * 32 + fr);
+#pragma unroll
+    for (int nb = 0; nb < WN; ++nb)
+      sw[nb][0] = FC1 ? word(1 + nb, prow0 / 2 + fr) : word(1, prow0 + 32 * nb + fr);
     frag(0, 0);
 #pragma unroll
+    for (int mb = 0; mb < WM; ++mb) mx4_spread(sa[mb][0], sa[mb]);
+#pragma unroll
+    for (int nb = 0; nb < WN; ++nb) mx4_spread(sw[nb][0], sw[nb]);
+#pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      if (ks == 2 && two) break;
+      // the row's last word: two slices
+      if (decltype(last)::value && ks == 2 && 2 * kt + 1 >= src.KB / 64) break;
       if (ks < 2) issue(cur ^ 1, ks);
       if (ks + 1 < 4) frag(ks + 1, (ks + 1) & 1);
+      // the next slice's reads stay ahead of this one's MFMAs
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int mb = 0; mb < WM; ++mb) {
         if (GUARD && mb >= nmb) continue;
@@ -1292,19 +1307,23 @@ __device__ __forceinline__ void mainloop_mx4(char* smem, const char* scales, con
                     op(wf[ks & 1][nb]), op(af[ks & 1][mb]), acc[mb][nb], 4, 4, 0,
                     (int)sw[nb][ks >> 1], 0, (int)sa[mb][ks >> 1]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
+  wait_vm(pend);
   int kt = kb;
-  for (; kt + 1 < ke; ++kt)
-    step(kt, [&](int st, int ks) {
+  for (; kt + 1 < ke; ++kt) {
+    step(kt, std::false_type{}, [&](int st, int ks) {
       issue_loads<HALF ? 2 : 4>(ld, lds0 + st * STAGE_BYTES, kt + 1, ks);
-      if (ks == 1) src.template issue_scales<FC1>(t, kt + 1, scl0 + st * MX4_SCALES);
+      if (ks == 0) src.issue_words(words, kt + 1, scl0 + st * MX4_SCALES);
     });
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
   const TileLoads nxt = src.template loads<FC1>(nt);   // nt is this tile without a next one
-  step(kt, [&](int st, int ks) {
+  step(kt, std::true_type{}, [&](int st, int ks) {
     if (!has_next) return;
     issue_loads(nxt, lds0 + st * STAGE_BYTES, nkb, ks);
-    if (ks == 1) src.template issue_scales<FC1>(nt, nkb, scl0 + st * MX4_SCALES);
+    if (ks == 0) src.issue_words(src.template words<FC1>(nt), nkb, scl0 + st * MX4_SCALES);
   });
 }
 
