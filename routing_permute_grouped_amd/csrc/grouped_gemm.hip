@@ -96,6 +96,16 @@ __device__ __forceinline__ void store4(bf16_t* p, float a, float b, float c, flo
 //          tw null: 1):
 //          [w*u*b*silu'(a) | w*u*silu(a)] -> C [m][2N], w*silu(a)*b -> dh [m][N], and the
 //          row's sums of u*silu(a)*b over each 64 columns -> dots [N/64][m_cap] when set
+// The eight waves' parts of a tile: 128 (a half tile: 64) rows x 64 panel rows each, two by
+// four; of a narrow one (half a tile's rows and half its panel) 32 x 64, four by two.
+template <bool HALF, bool NARROW>
+struct Waves {
+  static constexpr int rows = NARROW ? 32 : HALF ? 64 : 128;
+  static constexpr int blocks = rows / 32;
+  __device__ static int row0(int wave) { return NARROW ? (wave & 3) * 32 : (wave & 1) * rows; }
+  __device__ static int col(int wave) { return NARROW ? wave >> 2 : wave >> 1; }   // 64 panel rows
+};
+
 enum Mode { kFc1 = 0, kFc2 = 1, kDgrad = 2, kFc1Q = 3, kDgradQ = 4 };
 constexpr bool is_fc1(int mode) { return mode == kFc1 || mode == kFc1Q; }
 
@@ -444,18 +454,19 @@ __device__ __forceinline__ bf16x8 frag_mn(const char* stage, int nbase, int ks) 
 //
 // GUARD: the tile's rows from `vrows` on hold no token (pad rows, read as zeros): a
 // wave runs no MFMA for its 32-row blocks that lie wholly among them.
-template <bool HALF, bool A_MN, bool P_MN, bool GUARD = false>
+template <bool HALF, bool A_MN, bool P_MN, bool GUARD = false, bool NARROW = false>
 __device__ __forceinline__ void mainloop(char* smem, const TileLoads& ld, int kb, int ke,
                                          int stage0, bool primed, const TileLoads& nxt,
-                                         bool has_next, int nkb, f32x16 (&acc)[HALF ? 2 : 4][2],
+                                         bool has_next, int nkb,
+                                         f32x16 (&acc)[Waves<HALF, NARROW>::blocks][2],
                                          int vrows = BM) {
-  constexpr int WM = HALF ? 2 : 4;   // 32-row blocks of A per wave
+  constexpr int WM = Waves<HALF, NARROW>::blocks;   // 32-row blocks of A per wave
   constexpr int WN = 2;              // 32-row panel blocks per wave
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int arow0 = (wave & 1) * (HALF ? 64 : 128);   // first A row of this wave
-  const int prow0 = (wave >> 1) * 64;                 // first panel row of this wave
+  const int arow0 = Waves<HALF, NARROW>::row0(wave);      // first A row of this wave
+  const int prow0 = Waves<HALF, NARROW>::col(wave) * 64;  // first panel row of this wave
   const uint32_t lds0 = lds_addr(smem) + wave * 1024;
   const int nmb = GUARD ? max(0, min(WM, (vrows - arow0 + 31) >> 5)) : WM;
 
@@ -689,13 +700,13 @@ __device__ __forceinline__ void fc2_epilogue(char* lo, char* hi, const Tile& t, 
 
 // kFc1Q epilogue, straight from the accumulators: the wave's w1 and w3 sums of 32 columns
 // are one MX block each of [a | b] per row.
-template <bool HALF>
+template <bool HALF, bool NARROW = false>
 __device__ __forceinline__ void fc1q_epilogue(const Tile& t, const Epi& ep,
-                                              const f32x16 (&acc)[HALF ? 2 : 4][2]) {
-  constexpr int WM = HALF ? 2 : 4;
+                                              const f32x16 (&acc)[Waves<HALF, NARROW>::blocks][2]) {
+  constexpr int WM = Waves<HALF, NARROW>::blocks;
   const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int N = ep.N, n = t.n0 + (wave >> 1) * 32;
+  const int N = ep.N, n = t.n0 + Waves<HALF, NARROW>::col(wave) * 32;
   if (n >= N) return;   // N is a multiple of 64: a block of 32 columns is in or out
   const size_t m0 = t.m0;
   const rows_t rq = tile_rows(ep.q + m0 * 2 * N, t.rows * 2 * N);
@@ -705,7 +716,7 @@ __device__ __forceinline__ void fc1q_epilogue(const Tile& t, const Epi& ep,
   const int os = fr * (N / 16) + half * (N / 32);   // half 0 stores a's byte, half 1 b's
 #pragma unroll
   for (int mb = 0; mb < WM; ++mb) {
-    const int r = (wave & 1) * (HALF ? 64 : 128) + mb * 32;
+    const int r = Waves<HALF, NARROW>::row0(wave) + mb * 32;
     const f32x16 &a = acc[mb][0], &b = acc[mb][1];
     const uint32_t sa = quantize_run16(a, rq, oq + (r * 2 * N + n));
     const uint32_t sb = quantize_run16(b, rq, oq + (r * 2 * N + N + n));
@@ -729,9 +740,9 @@ __device__ __forceinline__ void fc1q_epilogue(const Tile& t, const Epi& ep,
 struct Slots {
   int s[2];
 };
-template <bool HALF>
+template <bool HALF, bool NARROW = false>
 __device__ __forceinline__ Slots wave_slots(const Tile& t, const Epi& ep) {
-  const int r = (int)((threadIdx.x >> 6) & 1) * (HALF ? 64 : 128) + (int)(threadIdx.x & 63);
+  const int r = Waves<HALF, NARROW>::row0((int)(threadIdx.x >> 6)) + (int)(threadIdx.x & 63);
   Slots o{{-1, -1}};
   if (ep.tw) {   // uniform
     const rows_t rr = tile_rows(ep.src + t.m0, t.vrows * 4);   // rows past the tokens get weight 0
@@ -740,20 +751,20 @@ __device__ __forceinline__ Slots wave_slots(const Tile& t, const Epi& ep) {
   }
   return o;
 }
-template <bool HALF>
+template <bool HALF, bool NARROW = false>
 __device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep, const Slots& slots,
-                                                const f32x16 (&acc)[HALF ? 2 : 4][2]) {
-  constexpr int WM = HALF ? 2 : 4;
+                                                const f32x16 (&acc)[Waves<HALF, NARROW>::blocks][2]) {
+  constexpr int WM = Waves<HALF, NARROW>::blocks;
   const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int N = ep.N, n0 = t.n0 + (wave >> 1) * 64;
+  const int N = ep.N, n0 = t.n0 + Waves<HALF, NARROW>::col(wave) * 64;
   if (n0 >= N) return;   // N is a multiple of 64
   const size_t m0 = t.m0;
   const rows_t rq = tile_rows(ep.q + m0 * 2 * N, t.vrows * 2 * N);
   const rows_t rs = tile_rows(ep.qs + m0 * (N / 16), t.vrows * (N / 16));
   const rows_t rc = tile_rows(ep.C + m0 * 2 * N, t.rows * 4 * N);
   const rows_t rh = tile_rows(ep.dh + m0 * N, t.rows * 2 * N);
-  const int w0 = (wave & 1) * (HALF ? 64 : 128);   // the wave's first row
+  const int w0 = Waves<HALF, NARROW>::row0(wave);   // the wave's first row
   const int oq = fr * 2 * N + 16 * half, os = fr * (N / 16), oc = 2 * oq;
   const int oh = (fr * N + 16 * half) * 2;
 
@@ -831,12 +842,12 @@ __device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep, co
 }
 
 // Pad rows' sums to zero: their zero rows against an infinite or NaN weight would give NaN.
-template <bool HALF>
-__device__ __forceinline__ void zero_pads(const Tile& t, f32x16 (&acc)[HALF ? 2 : 4][2]) {
+template <bool HALF, bool NARROW = false>
+__device__ __forceinline__ void zero_pads(const Tile& t, f32x16 (&acc)[Waves<HALF, NARROW>::blocks][2]) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-  for (int mb = 0; mb < (HALF ? 2 : 4); ++mb) {
-    const int r = (wave & 1) * (HALF ? 64 : 128) + 32 * mb;
+  for (int mb = 0; mb < Waves<HALF, NARROW>::blocks; ++mb) {
+    const int r = Waves<HALF, NARROW>::row0(wave) + 32 * mb;
     if (r + 32 <= t.vrows) continue;
     const bool pad = r + (int)(threadIdx.x & 31) >= t.vrows;
 #pragma unroll
@@ -931,18 +942,24 @@ __device__ __forceinline__ void finish_tile(char* smem, const Tile& t, const Epi
 }
 
 // One tile of the m-grouped kernel: the main loop, then finish_tile.
-template <int MODE, bool HALF, bool P_MN, bool GUARD = false>
+template <int MODE, bool HALF, bool P_MN, bool GUARD = false, bool NARROW = false>
 __device__ __forceinline__ void run_tile(char* smem, const Tile& t, const TileLoads& ld,
                                          const Epi& ep, int kb, int ke,
                                          float* __restrict__ part, int stage0, bool primed,
                                          const TileLoads& nxt, bool has_next, int nkb) {
-  f32x16 acc[HALF ? 2 : 4][2];
+  f32x16 acc[Waves<HALF, NARROW>::blocks][2];
   Slots slots{};
-  if (MODE == kDgradQ) slots = wave_slots<HALF>(t, ep);
-  mainloop<HALF, false, P_MN, GUARD>(smem, ld, kb, ke, stage0, primed, nxt, has_next, nkb, acc,
+  if (MODE == kDgradQ) slots = wave_slots<HALF, NARROW>(t, ep);
+  mainloop<HALF, false, P_MN, GUARD, NARROW>(smem, ld, kb, ke, stage0, primed, nxt, has_next, nkb, acc,
                                      t.vrows);
-  if (MODE >= kFc1Q && GUARD) zero_pads<HALF>(t, acc);
-  finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc, nullptr, nullptr, slots);
+  if (MODE >= kFc1Q && GUARD) zero_pads<HALF, NARROW>(t, acc);
+  if constexpr (NARROW) {   // never cut over k
+    if constexpr (MODE == kFc1Q) fc1q_epilogue<HALF, NARROW>(t, ep, acc);
+    else dgradq_epilogue<HALF, NARROW>(t, ep, slots, acc);
+    return;
+  } else {
+    finish_tile<MODE, HALF>(smem, t, ep, kb, ke, part, stage0, acc, nullptr, nullptr, slots);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1480,9 +1497,12 @@ __device__ Tile decode_item(const Sched& sc, int E, int n_nt, int cols, int w, i
 // min_saved: a tile is cut only if that saves at least so many k-steps of the round. The
 // 4-bit products and the checkpoint's two GEMMs ask for 20: writing, reading and adding the
 // shares costs 7 to 15 us, and a reduction that finds nothing to add 4. (Cut against uncut in
-// halved row blocks, 200 tokens of one expert, 2048 columns: fc1 with the checkpoint, D = 1024
-// (14 steps saved) 36.3 against 25.9 us, D = 2048 (28) 36.2 against 37.1; 4-bit fc2, F = 4096
-// (14) 27.4 against 25.3 us, F = 8192 (28) 30.4 against 40.6.)
+// halved row blocks, 200 tokens of one expert, 2048 columns: 4-bit fc2, F = 4096 (14 steps
+// saved) 27.4 against 25.3 us, F = 8192 (28) 30.4 against 40.6.) Few tiles of the checkpoint's
+// GEMMs are better made smaller (plan_rows) up to 50 steps saved for fc1, 30 for its backward:
+// fc1 of that expert, D = 2048 (28) 36.4 against 29.3 us, D = 4096 (56) 42.8 against 46.1; the
+// backward, 1500 tokens top-2 over 8 experts, F = 1024, D = 2048 (24) 51.2 against 43.2, D =
+// 4096 (48) 62.9 against 67.4.
 constexpr int kMinSaved = 20;
 
 struct Split {
@@ -1490,10 +1510,12 @@ struct Split {
 };
 
 constexpr int min_saved(int mode) { return mode >= kFc1Q ? kMinSaved : 0; }
+constexpr int few_saved(int mode) { return mode == kFc1Q ? 50 : mode == kDgradQ ? 30 : 0; }
 // Whether a GEMM of nk k-steps can cut its last round at all (at most 8 shares).
-constexpr bool may_split(int nk) { return nk - (nk + 7) / 8 >= kMinSaved; }
+constexpr bool may_split(int nk, int saved = kMinSaved) { return nk - (nk + 7) / 8 >= saved; }
 
-__device__ Split split_plan(int total, int G, int slots, int nk, int min_saved) {
+__device__ Split split_plan(int total, int G, int slots, int nk, int min_saved,
+                            int min_saved_few = 0) {
   Split p;
   const int rounds = (total + G - 1) / G;
   p.full = total;
@@ -1506,7 +1528,7 @@ __device__ Split split_plan(int total, int G, int slots, int nk, int min_saved) 
     int S = min(min(8, G / tail), min(slots / tail, nk));
     const int nks = (nk + S - 1) / S;
     S = (nk + nks - 1) / nks;   // no empty share
-    if (S >= 2 && nk - nks >= min_saved) {
+    if (S >= 2 && nk - nks >= (2 * total <= G ? max(min_saved, min_saved_few) : min_saved)) {
       p.full = (rounds - 1) * G;
       p.tail = tail;
       p.S = S;
@@ -1521,8 +1543,10 @@ __device__ Split split_plan(int total, int G, int slots, int nk, int min_saved) 
 // a tile. (Halves against whole tiles, 1500 tokens top-2 over 8 experts, F = 1024: fc1 with the
 // checkpoint, D = 1024 29.9 against 39.0 us; its backward, D = 512 29.8 against 39.7; 4-bit
 // fc1, D = 4096 28.0 against 36.7. Halves against a cut in two: 4-bit fc1, D = 8192 46.1 against
-// 57.1 us; against a cut in four: the backward, D = 2048 51.4 against 50.7, D = 4096 80.3 against
-// 62.9.)
+// 57.1 us.) Where that still leaves half of them idle, the checkpoint's GEMMs halve the columns
+// as well: their epilogues are long, and the panel's unused half is loaded only to keep the
+// loads as they are (389 tokens top-2 over 8 experts, D = 512, F = 1088: fc1 21.5 -> 17.1 us,
+// the backward 29.9 -> 24.9).
 __device__ __forceinline__ bool may_halve(const Split& sp, int total, int G) {
   return 2 * total <= G && sp.S <= 2;
 }
@@ -1536,11 +1560,20 @@ __device__ bool tall_rows(const Sched& sc, int E) {
 }
 
 // The block height for the plan sp of `total` tiles, and the plan and the tiles of that height.
-__device__ __forceinline__ int plan_rows(Sched& sc, int E, int n_nt, int total, int nk, Split& sp) {
-  if (!may_halve(sp, total, gridDim.x) || !tall_rows(sc, E)) return BM;
-  sched_blocks(sc, E, BM / 2);
-  sp = Split{sc.tstart[E] * n_nt, 0, 1, nk};
-  return BM / 2;
+// narrow: all tiles are of half height, and of half the width still no more than the workgroups.
+struct Blocks {
+  int bm;
+  bool narrow;
+};
+__device__ __forceinline__ Blocks plan_rows(Sched& sc, int E, int n_nt, int total, int nk,
+                                            Split& sp) {
+  if (!may_halve(sp, total, gridDim.x)) return Blocks{BM, false};
+  const bool tall = tall_rows(sc, E);
+  if (tall) {
+    sched_blocks(sc, E, BM / 2);
+    sp = Split{sc.tstart[E] * n_nt, 0, 1, nk};
+  }
+  return Blocks{tall ? BM / 2 : BM, sp.tail == 0 && 2 * sp.full <= (int)gridDim.x};
 }
 
 // P_MN: the weights are read MN-major (see tile_loads); ksplit as there. MX: fc1 on the
@@ -1556,12 +1589,20 @@ __global__ __launch_bounds__(NTHR, 1) void gg_bf16_kernel(
   __shared__ Sched sc;
   build_sched(sc, sg, E, m_cap);
 
-  const int cols = FC1 ? BP / 2 : BP;
-  const int n_nt = (N + cols - 1) / cols;
+  int cols = FC1 ? BP / 2 : BP;
+  int n_nt = (N + cols - 1) / cols;
   const int total = sc.tstart[E] * n_nt;
   const int nk = K * EB / (BK * 2);   // 128-byte k-steps
-  Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE));
-  const int bm = MODE >= kFc1Q ? plan_rows(sc, E, n_nt, total, nk, sp) : BM;
+  Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE), few_saved(MODE));
+  Blocks bl{BM, false};
+  if (MODE >= kFc1Q) {
+    bl = plan_rows(sc, E, n_nt, total, nk, sp);
+    if (bl.narrow) {
+      cols /= 2;
+      n_nt = (N + cols - 1) / cols;
+      sp.full = sc.tstart[E] * n_nt;
+    }
+  }
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
   if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
@@ -1585,7 +1626,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_bf16_kernel(
       r.ke = min(nk, r.kb + sp.nks);
       r.part = ws + (size_t)j * (BM * BP);
     }
-    r.t = decode_item(sc, E, n_nt, cols, tile, bm);
+    r.t = decode_item(sc, E, n_nt, cols, tile, bl.bm);
     return r;
   };
 
@@ -1624,6 +1665,13 @@ __global__ __launch_bounds__(NTHR, 1) void gg_bf16_kernel(
     }
     // a tile whose token rows end inside it skips the MFMAs of its pad-row blocks
     const bool guard = cur.t.vrows < cur.t.rows;
+    if constexpr (MODE >= kFc1Q) {
+      if (bl.narrow) {   // one tile a workgroup
+        run_tile<MODE, true, P_MN, true, true>(smem, cur.t, ld, ep, 0, nk, nullptr, stage0, primed,
+                                               nl, has_next, nw.kb);
+        return;
+      }
+    }
     if (cur.t.rows > BM / 2) {
       if (guard)
         run_tile<MODE, false, P_MN, true>(smem, cur.t, ld, ep, cur.kb, cur.ke, cur.part, stage0,
@@ -1666,7 +1714,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_mx4_kernel(const bf16_t* __restric
   const int total = sc.tstart[E] * n_nt;
   const int nk = (KB + 127) / 128;
   Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, kMinSaved);
-  const int bm = plan_rows(sc, E, n_nt, total, nk, sp);
+  const int bm = plan_rows(sc, E, n_nt, total, nk, sp).bm;
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
   if (gridDim.x % XCDS == 0) vb = (blockIdx.x % XCDS) * (gridDim.x / XCDS) + blockIdx.x / XCDS;
@@ -1810,18 +1858,18 @@ struct RingPos {
 // panel pieces of step s+2 are the last vector-memory instructions it issues in step s,
 // so the wait at the top of step s+1 leaves exactly those 4 in flight. Returns the
 // next tile's bpre.
-template <bool HALF>
+template <bool HALF, bool NARROW = false>
 __device__ __forceinline__ int mainloop_ring(char* smem, const TileLoads& ld, int kb, int ke,
                                              RingPos p0, bool aprimed, int bpre,
                                              const TileLoads& nxt, bool has_next, int nkb,
-                                             int nn, f32x16 (&acc)[HALF ? 2 : 4][2]) {
-  constexpr int WM = HALF ? 2 : 4;
+                                             int nn, f32x16 (&acc)[Waves<HALF, NARROW>::blocks][2]) {
+  constexpr int WM = Waves<HALF, NARROW>::blocks;
   constexpr int WN = 2;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = tid >> 6;
-  const int arow0 = (wave & 1) * (HALF ? 64 : 128);
-  const int prow0 = (wave >> 1) * 64;
+  const int arow0 = Waves<HALF, NARROW>::row0(wave);
+  const int prow0 = Waves<HALF, NARROW>::col(wave) * 64;
   const uint32_t lds0 = lds_addr(smem) + wave * 1024;
   const uint32_t ldsb = lds0 + 2 * A_BYTES - A_BYTES;   // issue_loads adds A_BYTES for the panel
 
@@ -1899,17 +1947,25 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
   int nblk;
   SchedR sr = build_sched_r(sg, E, m_cap, nblk);
 
-  const int cols = FC1 ? BP / 2 : BP;
-  const int n_nt = (N + cols - 1) / cols;
+  int cols = FC1 ? BP / 2 : BP;
+  int n_nt = (N + cols - 1) / cols;
   const int total = nblk * n_nt;
   const int nk = K / BK;
-  Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE));
+  Split sp = split_plan(total, gridDim.x, ws ? slots : 0, nk, min_saved(MODE), few_saved(MODE));
   int bm = BM;   // as plan_rows
-  if (MODE >= kFc1Q && may_halve(sp, total, gridDim.x) &&
-      __ballot(sr.end - sr.off > BM / 2) != 0) {
-    bm = BM / 2;
-    sched_blocks_r(sr, bm, nblk);
-    sp = Split{nblk * n_nt, 0, 1, nk};
+  bool narrow = false;
+  if (MODE >= kFc1Q && may_halve(sp, total, gridDim.x)) {
+    if (__ballot(sr.end - sr.off > BM / 2) != 0) {
+      bm = BM / 2;
+      sched_blocks_r(sr, bm, nblk);
+      sp = Split{nblk * n_nt, 0, 1, nk};
+    }
+    narrow = sp.tail == 0 && 2 * sp.full <= (int)gridDim.x;
+    if (narrow) {
+      cols /= 2;
+      n_nt = (N + cols - 1) / cols;
+      sp.full = nblk * n_nt;
+    }
   }
   const int items = sp.full + sp.tail * sp.S;
   int vb = blockIdx.x;
@@ -1958,6 +2014,15 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
     char* elo = smem + ((p.a + nlast) & 1) * A_BYTES;
     char* ehi = smem + 2 * A_BYTES + ((p.b + nlast) % 3) * B_BYTES;
     int nbp;
+    if constexpr (MODE == kFc1Q) {
+      if (narrow) {   // one tile a workgroup
+        f32x16 acc[1][2];
+        mainloop_ring<true, true>(smem, ld, 0, nk, p, aprimed, bpre, nl, has_next, nw.kb, nn, acc);
+        if (cur.t.vrows < cur.t.rows) zero_pads<true, true>(cur.t, acc);
+        fc1q_epilogue<true, true>(cur.t, ep, acc);
+        return;
+      }
+    }
     if (cur.t.rows > BM / 2) {
       f32x16 acc[4][2];
       nbp = mainloop_ring<false>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
@@ -1994,7 +2059,7 @@ __global__ __launch_bounds__(256) void gg_tail_reduce(Segs sg, int E, int K, int
   const int cols = FC1 ? BP / 2 : BP;
   const int n_nt = (N + cols - 1) / cols;
   const int total = sc.tstart[E] * n_nt;
-  const Split sp = split_plan(total, G, slots, K / BK, min_saved);
+  const Split sp = split_plan(total, G, slots, K / BK, min_saved, few_saved(MODE));
   if (sp.tail == 0) return;
   if (min_saved > 0 && may_halve(sp, total, G) && tall_rows(sc, E)) return;   // as plan_rows
   constexpr int Q = (FC1 ? BP / 2 : BP) / 4;   // 4-column groups per row
@@ -2594,15 +2659,22 @@ size_t ckpt8_scratch_bytes(int F, int64_t m_cap) {
   return (size_t)m_cap * (F / 64) * sizeof(float);
 }
 
+// Workspace slots of a checkpoint GEMM of n_nt column tiles: none where no call of these sizes
+// can cut a tile, which also saves the reduction's launch.
+static int ckpt8_slots(int mode, int E, int K, int n_nt, int64_t m_cap, const void* ws,
+                       size_t ws_bytes) {
+  const int64_t most = (m_cap / BM + std::min<int64_t>(E, m_cap / 16)) * n_nt;   // tiles
+  if (!ws || !may_split(K / BK, 2 * most <= cu_count() ? few_saved(mode) : kMinSaved)) return 0;
+  return (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20);
+}
+
 hipError_t launch_grouped_fc1_ckpt8(const void* x_perm, const int32_t* offsets,
                                     const int32_t* counts, int E, int D, int F, int64_t m_cap,
                                     const void* w1, const void* w3, void* h, void* q, void* qs,
                                     void* workspace, size_t ws_bytes, hipStream_t s) {
   const int G = cu_count(), mc = (int)m_cap;
   float* ws = static_cast<float*>(workspace);
-  const int slots = ws && may_split(D / BK)
-                        ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20)
-                        : 0;
+  const int slots = ckpt8_slots(kFc1Q, E, D, (F + BP / 2 - 1) / (BP / 2), m_cap, ws, ws_bytes);
   const Segs sg{offsets, counts, 0};
   const Epi ep{static_cast<bf16_t*>(h), nullptr, nullptr, F, static_cast<uint8_t*>(q),
                static_cast<uint8_t*>(qs), nullptr, nullptr, 0, nullptr, mc};
@@ -2629,9 +2701,7 @@ hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offs
                                       size_t ws_bytes, hipStream_t s) {
   const int G = cu_count(), mc = (int)m_cap;
   float* ws = static_cast<float*>(workspace);
-  const int slots = ws && may_split(D / BK)
-                        ? (int)std::min<size_t>(ws_bytes / (BM * BP * sizeof(float)), 1 << 20)
-                        : 0;
+  const int slots = ckpt8_slots(kDgradQ, E, D, (F + BP - 1) / BP, m_cap, ws, ws_bytes);
   const Segs sg{offsets, counts, 0};
   float* dots = dtopk_w ? static_cast<float*>(scratch) : nullptr;
   const Epi ep{static_cast<bf16_t*>(dab), nullptr, static_cast<bf16_t*>(hw), F,

@@ -54,6 +54,9 @@ SHAPES = {   # counts, mt, D, F
     "whole_row_blocks": ([300, 257] * 7 + [256, 129], 64, 192, 1088),   # tiles for half the card
     "cut_in_two": ([100] * 8, 64, 2560, 1408),                # the backward: in six
     "halves_for_a_cut_in_two": ([2000], 64, 2560, 1408),      # the backward: cut in five
+    "narrow_with_a_rest": ([100, 7, 0, 250], 32, 128, 320),   # halved columns: 64 left over
+    "narrow_many_experts": ([9, 0] * 40, 16, 64, 192),
+    "shares_of_few_tiles": ([130, 90], 64, 4160, 448),
 }
 
 
