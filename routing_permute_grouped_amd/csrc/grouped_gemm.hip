@@ -16,7 +16,8 @@
 //   * eight waves, two per SIMD; on a full tile each wave owns 128 rows x 64 panel rows
 //     (8 MFMA blocks, 128 accumulators). A half tile (the last 128 rows of a segment
 //     whose length is an odd number of 128-row tiles) is split 64 rows x 64 panel rows
-//     per wave, so all four SIMDs stay busy.
+//     per wave, so all four SIMDs stay busy. The checkpoint's GEMMs also have tiles of 128
+//     rows x 128 panel rows, 32 x 64 a wave, for calls of few tiles (plan_rows).
 //   * an operand whose k is contiguous in memory is staged as 128-byte LDS rows with the
 //     16-byte chunk index XOR-swizzled by half the row index; an operand stored [k][n]
 //     (w2 read by the dgrad of fc2, w1/w3 by the dgrad of fc1, the activations by the
@@ -96,6 +97,9 @@ __device__ __forceinline__ void store4(bf16_t* p, float a, float b, float c, flo
 //          tw null: 1):
 //          [w*u*b*silu'(a) | w*u*silu(a)] -> C [m][2N], w*silu(a)*b -> dh [m][N], and the
 //          row's sums of u*silu(a)*b over each 64 columns -> dots [N/64][m_cap] when set
+enum Mode { kFc1 = 0, kFc2 = 1, kDgrad = 2, kFc1Q = 3, kDgradQ = 4 };
+constexpr bool is_fc1(int mode) { return mode == kFc1 || mode == kFc1Q; }
+
 // The eight waves' parts of a tile: 128 (a half tile: 64) rows x 64 panel rows each, two by
 // four; of a narrow one (half a tile's rows and half its panel) 32 x 64, four by two.
 template <bool HALF, bool NARROW>
@@ -105,9 +109,6 @@ struct Waves {
   __device__ static int row0(int wave) { return NARROW ? (wave & 3) * 32 : (wave & 1) * rows; }
   __device__ static int col(int wave) { return NARROW ? wave >> 2 : wave >> 1; }   // 64 panel rows
 };
-
-enum Mode { kFc1 = 0, kFc2 = 1, kDgrad = 2, kFc1Q = 3, kDgradQ = 4 };
-constexpr bool is_fc1(int mode) { return mode == kFc1 || mode == kFc1Q; }
 
 struct Epi {
   bf16_t* C;
@@ -733,7 +734,9 @@ __device__ __forceinline__ void fc1q_epilogue(const Tile& t, const Epi& ep,
 // columns with their codes (16 bytes of a and of b a lane) and scales, read one block of rows
 // ahead. The products of a row's 64 columns are summed in the lane, then over the two lane
 // halves. About 100 cycles of vector arithmetic an element of the wave, 32 of them in the
-// sigmoid's exponential and reciprocal: 11 us of a full tile, against 60 for its 32 k-steps.
+// sigmoid's exponential and reciprocal: 11 us of a full tile, against 60 for its 32 k-steps (8192
+// tokens top-6 over 64 experts, D = 2048, F = 1408: 478 us, 345 without the epilogue). Stores of
+// whole 64-byte pieces gained 3% before the lane swaps they take, non-temporal ones lost 13%.
 //
 // Slots: the slots of the wave's rows, one or two a lane, asked for before the main loop so
 // that only the weights' own load is left to wait for here.
@@ -1180,7 +1183,15 @@ __device__ __forceinline__ void run_tile_mx(char* smem, const Tile& t, const Epi
 //     registers of every wave that needs them (six a wave and step) they cost 6 to 19%;
 //   * the epilogue stores straight from the accumulators, without branches, so that a wave's
 //     stores are a known number and the next tile's first step can wait for its loads, which
-//     are older, and leave the stores in flight.
+//     are older, and leave the stores in flight;
+//   * a step's body has no branch but the last one's, and the next slice's LDS reads are held
+//     ahead of a slice's MFMAs: left to itself the compiler put the later slices' reads right
+//     before their use (fc1, 4096 tokens top-2 over 8 experts of D = 4096, F = 14336: 545 -> 523
+//     us; 32 experts of D = 7168, F = 512, 16200 rows: 99 -> 92).
+// The first of these runs at 1.6 to 1.7 GHz of 2.4 with the matrix cores busy in 47% of the
+// cycles: its MFMAs alone take 405 us, its loads and LDS reads alone 409, and together they
+// bring the clock down. Loads issued two steps ahead, which takes a second barrier a step,
+// were slower (586 us).
 // ---------------------------------------------------------------------------
 constexpr int MX4_SCALES = 6 * 1024;   // bytes of one stage's scale words
 
