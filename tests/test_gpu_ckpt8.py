@@ -311,6 +311,74 @@ def test_layer_forward_and_backward(name, split_k):
         assert np.isfinite(orc.values64(got)).all() and e <= P.TOL["bf16"], f"{key}: rel err {e:.3e}"
 
 
+@pytest.mark.parametrize("T", [1, 2, 129])
+def test_a_token_gives_the_same_bits_alone_and_in_a_batch(T):
+    inp, cfg, d, kw, dout = layer_case("dense8")
+    w, dd = (d["w1"], d["w3"], d["w2"]), P.to_dev(dout)
+    got = []
+    for n in (dout.shape[0], T):
+        x = d["x"][:n].contiguous()
+        fwd = rpg.moe_layer(x, *w, cfg.k, cfg.m_tile, split_k=False, save_for_backward="mxfp8", **kw)
+        g = rpg.moe_layer_backward(fwd, dd[:n].contiguous(), x, *w, cfg.m_tile, split_k=False)
+        got.append((fwd["out"], g["dx"], g["dtopk_w"]))
+    for a, b in zip(*got):
+        assert torch.equal(a[:T], b)
+
+
+def test_checkpoint_past_32_bits():
+    # 65536 rows of 2 * 65536 codes: the second expert's rows give the bits they give alone
+    D, F, mt = 64, 65536, 16
+    counts = [65536, 5]
+    offs, te, m_cap = segments(counts, mt)
+    b = dict(dtype=torch.bfloat16, device="cuda")
+    x = torch.randn((m_cap, D), **b)
+    x[-11:] = 0
+    w1, w3 = (torch.randn((2, F, D), **b) / 8 for _ in range(2))
+    w2 = torch.randn((2, D, F), **b) / 256
+    cnt = P.to_dev(np.array(counts, dtype=np.int32))
+    src = torch.arange(m_cap, dtype=torch.int32, device="cuda")
+    src[-11:] = -1
+    tw = torch.rand((counts[0] + 5, 1), device="cuda")
+    dst = torch.arange(tw.shape[0], dtype=torch.int32, device="cuda").view(-1, 1)
+
+    def run(x, offs, te, w1, w3, w2, cnt, src, dst, tw, m_cap):
+        h, q, s = rpg.moe_grouped_fc1_swiglu_ckpt8(x, offs, te, w1, w3, mt, m_cap, counts=cnt)
+        dab, hw, dtw = rpg.moe_grouped_dgrad_swiglu_ckpt8(x, offs, te, w2, q, s, mt, m_cap, src_row=src,
+                                                          dst_row=dst, topk_w=tw, counts=cnt)
+        return [t[-16:].clone() for t in (h, q, s, dab, hw)] + [dtw[-5:].clone()]
+
+    two = run(x, P.to_dev(offs), P.to_dev(te), w1, w3, w2, cnt, src, dst, tw, m_cap)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    src1 = torch.arange(mt, **i32)
+    src1[5:] = -1
+    one = run(x[-16:].contiguous(), torch.tensor([0, 16], **i32), torch.zeros(1, **i32), w1[1:].contiguous(),
+              w3[1:].contiguous(), w2[1:].contiguous(), cnt[1:].contiguous(), src1,
+              torch.arange(5, **i32).view(-1, 1), tw[-5:].contiguous(), mt)
+    for a, b in zip(two, one):
+        assert torch.equal(a, b)
+    assert one[3].any() and torch.isfinite(one[3].float()).all()
+
+
+def test_backward_without_the_weight_gradient():
+    c = use_case(*SHAPES["half_and_full_tiles"])
+    dab, hw, _ = run_use(c, False)
+    t = [P.to_dev(c[n]) for n in ("d", "offs", "te", "w2", "q", "s", "src", "w")]
+    cnt = P.to_dev(np.array(c["counts"], dtype=np.int32))
+    E, D, F, m_cap = len(c["counts"]), c["D"], c["F"], c["m_cap"]
+    b = dict(dtype=torch.bfloat16, device="cuda")
+    o = (P.poison(torch.empty((m_cap, 2 * F), **b)), P.poison(torch.empty((m_cap, F), **b)))
+    ptr = lambda x: x.data_ptr()  # noqa: E731
+    st = rpg.lib.moe_grouped_dgrad_swiglu_ckpt8(
+        ptr(t[0]), ptr(t[1]), ptr(cnt), ptr(t[2]), E, D, F, c["mt"], m_cap, ptr(t[3]), ptr(t[4]),
+        ptr(t[5]), ptr(t[6]), None, ptr(t[7]), *c["w"].shape, ptr(o[0]), ptr(o[1]), None, None, 0, None,
+        0, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0
+    used = int(c["offs"][-1])
+    for got, ref in zip(o, (dab, hw)):
+        np.testing.assert_array_equal(P.to_host(got)[:used].view(np.uint8), ref[:used].view(np.uint8))
+
+
 def test_weight_gradient_against_differences():
     # <dout, out> of the layer is linear in the top-k weights: its difference quotient is
     # exact up to rounding. The outputs are bf16 (half a step 2^-8 of each, random in sign)

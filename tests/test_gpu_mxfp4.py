@@ -436,6 +436,73 @@ def test_masked_layer(name):
     assert P.rel_err(P.to_host(g["out"]), out) <= P.TOL["bf16"]
 
 
+@pytest.mark.parametrize("T", [1, 2, 129])
+def test_a_token_gives_the_same_bits_alone_and_in_a_batch(T):
+    inp, d, kw = layer_inputs(LAYERS["dense8"])
+    cfg = inp["cfg"]
+    mw = rpg.Mx4Weights.quantize(d["w1"], d["w3"], d["w2"])
+    full = rpg.moe_layer_mxfp4(d["x"], mw, cfg.k, cfg.m_tile, split_k=False, **kw)
+    few = rpg.moe_layer_mxfp4(d["x"][:T].contiguous(), mw, cfg.k, cfg.m_tile, split_k=False, **kw)
+    assert torch.equal(few["topk_idx"], full["topk_idx"][:T])
+    assert torch.equal(few["out"], full["out"][:T])
+
+
+# ---- sizes past 32 bits ---------------------------------------------------------------
+
+def same_bits(a, b):
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def codes_on_device(*shape):
+    """Random code bytes and words of middling scales for rows of shape[-1] bytes."""
+    q = torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda")
+    rows = q.numel() // shape[-1]
+    return q, torch.randint(118, 122, (shape[-1] // 64, rows, 4), dtype=torch.uint8, device="cuda")
+
+
+def test_rows_past_32_bits():
+    R, C = 70000, 65536          # 4.6e9 values
+    x = torch.zeros((R, C), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn((3, C), device="cuda").to(torch.bfloat16)
+    for layout in (ROWS, KSTEPS):
+        q, s = rpg.moe_quantize_mxfp4(x, layout=layout)
+        ref = rpg.moe_quantize_mxfp4(x[-3:].contiguous(), layout=layout)
+        assert torch.equal(q[-3:], ref[0]) and not q[:3].any()
+        assert torch.equal(s[-3:] if layout == ROWS else s[:, -3:], ref[1])
+        v = rpg.moe_dequantize_mxfp4(q, s, layout=layout)
+        assert torch.equal(v[-3:], rpg.moe_dequantize_mxfp4(*ref, layout=layout)) and not v[:3].any()
+        del q, s, v
+
+
+def test_weights_past_32_bits():
+    # 160 experts, 4.7e9 bytes of codes a matrix: the last expert's rows give the bits its weights
+    # give alone
+    E, D, F, cap = 160, 4096, 14336, 16
+    w1q, w1s = codes_on_device(E, F, D // 2)
+    w2q, w2s = codes_on_device(E, D, F // 2)
+    last = lambda q, s: (q[-1:].contiguous(), s[:, -q.shape[1]:].contiguous())  # noqa: E731
+    one1, one2 = last(w1q, w1s), last(w2q, w2s)
+    x = torch.randn((E * cap, D), device="cuda").to(torch.bfloat16)
+    counts = torch.zeros(E, dtype=torch.int32, device="cuda")
+    counts[-1] = 5
+    h, y = rpg.moe_grouped_swiglu_masked_mxfp4(x, counts, w1q, w1s, w1q, w1s, w2q, w2s, cap)
+    h1, y1 = rpg.moe_grouped_swiglu_masked_mxfp4(x[-cap:].contiguous(), counts[-1:].contiguous(), *one1,
+                                                 *one1, *one2, cap)
+    assert torch.equal(h[-cap:][:5], h1[:5]) and torch.equal(y[-cap:][:5], y1[:5])
+    assert torch.isfinite(y1[:5].float()).all() and y1[:5].any()
+    xq, xs = rpg.moe_quantize_mxfp4(x[:cap].contiguous(), layout=KSTEPS)
+    hq, hs = rpg.moe_quantize_mxfp4(h1, layout=KSTEPS)
+    offs = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offs[-1] = cap
+    te = torch.full((1,), E - 1, dtype=torch.int32, device="cuda")
+    offs1, te1 = offs[-2:].contiguous(), torch.zeros_like(te)
+    a = rpg.moe_grouped_fc1_swiglu_mxfp4(xq, xs, offs, te, w1q, w1s, w1q, w1s, cap)
+    same_bits(a, rpg.moe_grouped_fc1_swiglu_mxfp4(xq, xs, offs1, te1, *one1, *one1, cap))
+    b = rpg.moe_grouped_fc2_mxfp4(hq, hs, offs, te, w2q, w2s, cap)
+    # rows behind the five hold whatever was in memory, NaN perhaps
+    same_bits(b, rpg.moe_grouped_fc2_mxfp4(hq, hs, offs1, te1, *one2, cap))
+
+
 # ---- how calls are made ---------------------------------------------------------------
 
 def test_calls_on_other_streams_and_two_at_once():
