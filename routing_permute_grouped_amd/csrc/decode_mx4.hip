@@ -255,10 +255,11 @@ __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X
   }
 }
 
-// Row groups of 64 of expert e (none past the last expert).
-__device__ __forceinline__ int row_groups(const int32_t* counts, int e, int E, int cap) {
-  return e < E ? (max(0, min(counts[e], cap)) + GROUP - 1) / GROUP : 0;
+// Rows of expert e (none past the last expert), and their row groups of 64.
+__device__ __forceinline__ int rows_of(const int32_t* counts, int e, int E, int cap) {
+  return e < E ? max(0, min(counts[e], cap)) : 0;
 }
+__device__ __forceinline__ int groups_of(int rows) { return (rows + GROUP - 1) / GROUP; }
 
 // Exclusive prefix sum over the wave; total: the whole sum.
 __device__ __forceinline__ int wave_scan(int v, int& total) {
@@ -292,12 +293,12 @@ __global__ __launch_bounds__(DW * 64, 4) void dec4_kernel(const bf16_t* __restri
   __shared__ __attribute__((aligned(1024))) char xs[XBYTES];
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) / 64;
-  int sum = 0, groups;
-  bool tall = false;   // an expert with more than 32 rows
+  int sum = 0, groups, mine = 0;   // mine: rows of the lane's (last) expert
+  bool tall = false;               // an expert with more than 32 rows
   for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    sum += row_groups(counts, e, E, cap);
-    tall |= e < E && min(counts[e], cap) > 32;
+    mine = rows_of(counts, lane * per + i, E, cap);
+    sum += groups_of(mine);
+    tall |= mine > 32;
   }
   const int start = wave_scan(sum, groups);
   // with at most one 64-column item a CU, two waves share 16 columns: twice the items, half
@@ -310,14 +311,17 @@ __global__ __launch_bounds__(DW * 64, 4) void dec4_kernel(const bf16_t* __restri
     const int grp = item / ncols;
     int e = last_lane(start, true, grp);
     int s = __builtin_amdgcn_readlane(start, e);
+    int n = __builtin_amdgcn_readlane(mine, e);
     if (per > 1) {   // the lane's experts, one a lane
       int all;
-      const int at = wave_scan(lane < per ? row_groups(counts, e * per + lane, E, cap) : 0, all);
+      const int c = lane < per ? rows_of(counts, e * per + lane, E, cap) : 0;
+      const int at = wave_scan(groups_of(c), all);
       const int l = last_lane(at, lane < per, grp - s);
       s += __builtin_amdgcn_readlane(at, l);
+      n = __builtin_amdgcn_readlane(c, l);
       e = e * per + l;
     }
-    const int n = max(0, min(counts[e], cap)), ng = (n + GROUP - 1) / GROUP;
+    const int ng = groups_of(n);
     const int local = item - s * ncols;
     const int base = local / (XCDS * ng) * XCDS, in = local - base * ng;
     const int width = min(XCDS, ncols - base);
