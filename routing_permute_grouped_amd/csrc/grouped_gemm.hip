@@ -96,7 +96,7 @@ __device__ __forceinline__ void store4(bf16_t* p, float a, float b, float c, flo
 //          from such a checkpoint and the row's weight w (tw[src[m]], 0 without a slot;
 //          tw null: 1):
 //          [w*u*b*silu'(a) | w*u*silu(a)] -> C [m][2N], w*silu(a)*b -> dh [m][N], and the
-//          row's sums of u*silu(a)*b over each 64 columns -> dots [N/64][m_cap] when set
+//          row's sums of u*silu(a)*b over each 64 columns -> dots [m_cap][N/64] when set
 enum Mode { kFc1 = 0, kFc2 = 1, kDgrad = 2, kFc1Q = 3, kDgradQ = 4 };
 constexpr bool is_fc1(int mode) { return mode == kFc1 || mode == kFc1Q; }
 
@@ -121,7 +121,6 @@ struct Epi {
   const float* tw;
   int nslots;
   float* dots;
-  int m_cap;
 };
 
 // ---- The 8-bit checkpoint of [a | b] --------------------------------------------------
@@ -802,7 +801,7 @@ __device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep, co
     }
     if (w0 + 64 * i + lane >= t.vrows) wl[i] = 0.0f;
   }
-  float* dots = ep.dots ? ep.dots + (size_t)(n0 >> 6) * ep.m_cap + m0 : nullptr;
+  float* dots = ep.dots ? ep.dots + m0 * (N >> 6) + (n0 >> 6) : nullptr;
 #pragma unroll
   for (int mb = 0; mb < WM; ++mb) {
     const int r = w0 + 32 * mb;
@@ -840,7 +839,7 @@ __device__ __forceinline__ void dgradq_epilogue(const Tile& t, const Epi& ep, co
       __builtin_amdgcn_sched_barrier(0);
     }
     dot += __shfl_xor(dot, 32);
-    if (dots && half == 0 && r + fr < t.rows) dots[r + fr] = dot;
+    if (dots && half == 0 && r + fr < t.rows) dots[(r + fr) * (N >> 6)] = dot;
   }
 }
 
@@ -2146,7 +2145,7 @@ __global__ __launch_bounds__(256) void gg_tail_reduce(Segs sg, int E, int K, int
       store4(ep.dh + row + n, hw[0], hw[1], hw[2], hw[3]);
 #pragma unroll
       for (int d = 1; d < 16; d <<= 1) dot += __shfl_xor(dot, d);
-      if (ep.dots && (n & 63) == 0) ep.dots[(size_t)(n >> 6) * ep.m_cap + m] = dot;
+      if (ep.dots && (n & 63) == 0) ep.dots[(row + n) >> 6] = dot;
     } else if (MODE == kDgrad && r >= t.vrows) {   // pad row: zeros, its [a | b] is never read
       const float z[4] = {0.f, 0.f, 0.f, 0.f};
       dgrad4(ep, (size_t)(t.m0 + r) * N, n, z, uint2{0u, 0u}, uint2{0u, 0u});
@@ -2644,26 +2643,21 @@ hipError_t launch_grouped_fc1_mx(const void* xq_perm, const void* xs_perm,
   return hipGetLastError();
 }
 
-// Each slot's sum of its row's partial sums, in column order; 0 for slots without a row.
+// Each slot's sum of its row's partial sums, eight lanes a slot, in a fixed order; 0 for slots
+// without a row. (A row's sums side by side, 49152 slots of 22: 9.4 -> 6.0 us.)
 __global__ __launch_bounds__(256) void row_dot_kernel(const int32_t* __restrict__ dst_row,
                                                       const float* __restrict__ dots, int nslots,
                                                       int m_cap, int parts,
                                                       float* __restrict__ out) {
-  const int s = blockIdx.x * 256 + threadIdx.x;
-  if (s >= nslots) return;
-  const int r = dst_row[s];
-  float sum[8] = {};   // eight loads in flight; the order is fixed
-  if (r >= 0 && r < m_cap) {
-    const float* d = dots + r;
-    int p = 0;
-    for (; p + 8 <= parts; p += 8)
+  const int64_t s = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 3;
+  const int l = threadIdx.x & 7;
+  const int r = s < nslots ? dst_row[s] : -1;
+  float sum = 0.0f;
+  if (r >= 0 && r < m_cap)
+    for (int p = l; p < parts; p += 8) sum += dots[(size_t)r * parts + p];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += d[(size_t)(p + i) * m_cap];
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (p + i < parts) sum[i] += d[(size_t)(p + i) * m_cap];
-  }
-  out[s] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor(sum, d);
+  if (l == 0 && s < nslots) out[s] = sum;
 }
 
 size_t ckpt8_scratch_bytes(int F, int64_t m_cap) {
@@ -2688,7 +2682,7 @@ hipError_t launch_grouped_fc1_ckpt8(const void* x_perm, const int32_t* offsets,
   const int slots = ckpt8_slots(kFc1Q, E, D, (F + BP / 2 - 1) / (BP / 2), m_cap, ws, ws_bytes);
   const Segs sg{offsets, counts, 0};
   const Epi ep{static_cast<bf16_t*>(h), nullptr, nullptr, F, static_cast<uint8_t*>(q),
-               static_cast<uint8_t*>(qs), nullptr, nullptr, 0, nullptr, mc};
+               static_cast<uint8_t*>(qs), nullptr, nullptr, 0, nullptr};
   const bf16_t* a = static_cast<const bf16_t*>(x_perm);
   const bf16_t *b1 = static_cast<const bf16_t*>(w1), *b3 = static_cast<const bf16_t*>(w3);
   if (use_ring(E, m_cap))
@@ -2717,7 +2711,7 @@ hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offs
   float* dots = dtopk_w ? static_cast<float*>(scratch) : nullptr;
   const Epi ep{static_cast<bf16_t*>(dab), nullptr, static_cast<bf16_t*>(hw), F,
                static_cast<uint8_t*>(const_cast<void*>(q)),
-               static_cast<uint8_t*>(const_cast<void*>(qs)), src_row, topk_w, nslots, dots, mc};
+               static_cast<uint8_t*>(const_cast<void*>(qs)), src_row, topk_w, nslots, dots};
   const bf16_t* w = static_cast<const bf16_t*>(w2);
   hipLaunchKernelGGL((gg_bf16_kernel<kDgradQ, true>), dim3(G), dim3(NTHR), 0, s,
                      static_cast<const bf16_t*>(dout_perm), sg, E, D, F, mc, w, w, D, ep, ws,
@@ -2726,7 +2720,7 @@ hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offs
     hipLaunchKernelGGL(gg_tail_reduce<kDgradQ>, dim3(4 * G), dim3(256), 0, s, sg, E, D, mc, G,
                        slots, ws, ep, kMinSaved);
   if (dtopk_w)
-    hipLaunchKernelGGL(row_dot_kernel, dim3((nslots + 255) / 256), dim3(256), 0, s, dst_row, dots,
+    hipLaunchKernelGGL(row_dot_kernel, dim3((unsigned)(((int64_t)nslots + 31) / 32)), dim3(256), 0, s, dst_row, dots,
                        nslots, mc, F / 64, dtopk_w);
   return hipGetLastError();
 }
