@@ -1509,10 +1509,10 @@ __device__ Tile decode_item(const Sched& sc, int E, int n_nt, int cols, int w, i
 // shares costs 7 to 15 us, and a reduction that finds nothing to add 4. (Cut against uncut in
 // halved row blocks, 200 tokens of one expert, 2048 columns: 4-bit fc2, F = 4096 (14 steps
 // saved) 27.4 against 25.3 us, F = 8192 (28) 30.4 against 40.6.) Few tiles of the checkpoint's
-// GEMMs are better made smaller (plan_rows) up to 50 steps saved for fc1, 30 for its backward:
-// fc1 of that expert, D = 2048 (28) 36.4 against 29.3 us, D = 4096 (56) 42.8 against 46.1; the
-// backward, 1500 tokens top-2 over 8 experts, F = 1024, D = 2048 (24) 51.2 against 43.2, D =
-// 4096 (48) 62.9 against 67.4.
+// GEMMs are better made smaller (plan_rows) up to 50 steps saved: fc1 of that expert, D = 2048
+// (28) 36.4 against 29.3 us, D = 4096 (56) 42.8 against 46.1; the backward, 1500 tokens top-2
+// over 8 experts, F = 1024, D = 4096 (48) 61.7 against 54.0; 389 tokens, F = 1088 (53) 42.6
+// against 50.4.
 constexpr int kMinSaved = 20;
 
 struct Split {
@@ -1520,7 +1520,7 @@ struct Split {
 };
 
 constexpr int min_saved(int mode) { return mode >= kFc1Q ? kMinSaved : 0; }
-constexpr int few_saved(int mode) { return mode == kFc1Q ? 50 : mode == kDgradQ ? 30 : 0; }
+constexpr int few_saved(int mode) { return mode >= kFc1Q ? 50 : 0; }
 // Whether a GEMM of nk k-steps can cut its last round at all (at most 8 shares).
 constexpr bool may_split(int nk, int saved = kMinSaved) { return nk - (nk + 7) / 8 >= saved; }
 
@@ -1556,7 +1556,7 @@ __device__ Split split_plan(int total, int G, int slots, int nk, int min_saved,
 // 57.1 us.) Where that still leaves half of them idle, the checkpoint's GEMMs halve the columns
 // as well: their epilogues are long, and the panel's unused half is loaded only to keep the
 // loads as they are (389 tokens top-2 over 8 experts, D = 512, F = 1088: fc1 21.5 -> 17.1 us,
-// the backward 29.9 -> 24.9).
+// the backward 29.9 -> 24.9, on the ring then 20.9).
 __device__ __forceinline__ bool may_halve(const Split& sp, int total, int G) {
   return 2 * total <= G && sp.S <= 2;
 }
@@ -1779,7 +1779,9 @@ __global__ __launch_bounds__(NTHR, 1) void gg_mx4_kernel(const bf16_t* __restric
 }
 
 // ---------------------------------------------------------------------------
-// Ring pipeline for the forward GEMMs (bf16, K-contiguous weights) with at most 64
+// Ring pipeline for the forward GEMMs (bf16, K-contiguous weights) and for the backward from
+// the checkpoint (w2 read MN-major; 8192 tokens top-6 over 64 experts 486 -> 471 us, 389 tokens
+// top-2 over 8, D = 512 24.5 -> 20.9, D = 2048 43 -> 34) with at most 64
 // experts: two activation slots and three weight-panel slots (160 KiB, all of the LDS),
 // so a panel is requested two k-steps before its use and the activations one step
 // before. The schedule tables live in registers: lane e holds expert e's segment bounds
@@ -1868,7 +1870,7 @@ struct RingPos {
 // panel pieces of step s+2 are the last vector-memory instructions it issues in step s,
 // so the wait at the top of step s+1 leaves exactly those 4 in flight. Returns the
 // next tile's bpre.
-template <bool HALF, bool NARROW = false>
+template <bool HALF, bool P_MN = false, bool NARROW = false>
 __device__ __forceinline__ int mainloop_ring(char* smem, const TileLoads& ld, int kb, int ke,
                                              RingPos p0, bool aprimed, int bpre,
                                              const TileLoads& nxt, bool has_next, int nkb,
@@ -1917,7 +1919,8 @@ __device__ __forceinline__ int mainloop_ring(char* smem, const TileLoads& ld, in
       const int chk = ks * 2 + (lane >> 5);
 #pragma unroll
       for (int nb = 0; nb < WN; ++nb)
-        wf[buf][nb] = *reinterpret_cast<const bf16x8*>(sb + swz(prow0 + nb * 32 + fr, chk));
+        wf[buf][nb] = P_MN ? frag_mn(sb, prow0 + nb * 32, ks)
+                           : *reinterpret_cast<const bf16x8*>(sb + swz(prow0 + nb * 32 + fr, chk));
 #pragma unroll
       for (int mb = 0; mb < WM; ++mb)
         af[buf][mb] = *reinterpret_cast<const bf16x8*>(sa + swz(arow0 + mb * 32 + fr, chk));
@@ -1951,8 +1954,8 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
     const bf16_t* __restrict__ A, Segs sg, int E, int K, int N, int m_cap,
     const bf16_t* __restrict__ W1, const bf16_t* __restrict__ W3, Epi ep,
     float* __restrict__ ws, int slots) {
-  static_assert(is_fc1(MODE) || MODE == kFc2, "the ring serves the forward GEMMs");
-  constexpr bool FC1 = is_fc1(MODE);
+  static_assert(is_fc1(MODE) || MODE == kFc2 || MODE == kDgradQ, "no LDS is left for others");
+  constexpr bool FC1 = is_fc1(MODE), P_MN = MODE == kDgradQ;
   __shared__ __attribute__((aligned(16))) char smem[RING_BYTES];
   int nblk;
   SchedR sr = build_sched_r(sg, E, m_cap, nblk);
@@ -2005,7 +2008,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
 
   if (vb >= items) return;
   Work cur = work(vb);
-  TileLoads ld = tile_loads<FC1, false, 2>(cur.t, A, W1, W3, K, N, K);
+  TileLoads ld = tile_loads<FC1, P_MN, 2>(cur.t, A, W1, W3, K, N, K);
   RingPos p{0, 0};
   bool aprimed = false;
   int bpre = 0;
@@ -2015,7 +2018,7 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
     TileLoads nl = ld;
     if (has_next) {
       nw = work(w + gridDim.x);
-      nl = tile_loads<FC1, false, 2>(nw.t, A, W1, W3, K, N, K);
+      nl = tile_loads<FC1, P_MN, 2>(nw.t, A, W1, W3, K, N, K);
     }
     const int nn = has_next ? nw.ke - nw.kb : 0;
     // free after the tile's last step: its activation slot and its panel slot (the next
@@ -2024,27 +2027,33 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
     char* elo = smem + ((p.a + nlast) & 1) * A_BYTES;
     char* ehi = smem + 2 * A_BYTES + ((p.b + nlast) % 3) * B_BYTES;
     int nbp;
-    if constexpr (MODE == kFc1Q) {
+    Slots rslots{};
+    if constexpr (MODE == kDgradQ)
+      rslots = cur.t.rows > BM / 2 ? wave_slots<false>(cur.t, ep)
+               : narrow            ? wave_slots<true, true>(cur.t, ep)
+                                   : wave_slots<true>(cur.t, ep);
+    if constexpr (MODE >= kFc1Q) {
       if (narrow) {   // one tile a workgroup
         f32x16 acc[1][2];
-        mainloop_ring<true, true>(smem, ld, 0, nk, p, aprimed, bpre, nl, has_next, nw.kb, nn, acc);
+        mainloop_ring<true, P_MN, true>(smem, ld, 0, nk, p, aprimed, bpre, nl, has_next, nw.kb, nn, acc);
         if (cur.t.vrows < cur.t.rows) zero_pads<true, true>(cur.t, acc);
-        fc1q_epilogue<true, true>(cur.t, ep, acc);
+        if constexpr (MODE == kFc1Q) fc1q_epilogue<true, true>(cur.t, ep, acc);
+        else dgradq_epilogue<true, true>(cur.t, ep, rslots, acc);
         return;
       }
     }
     if (cur.t.rows > BM / 2) {
       f32x16 acc[4][2];
-      nbp = mainloop_ring<false>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
+      nbp = mainloop_ring<false, P_MN>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
                                  nn, acc);
-      if (MODE == kFc1Q && cur.t.vrows < cur.t.rows) zero_pads<false>(cur.t, acc);
-      finish_tile<MODE, false>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, 0, acc, elo, ehi);
+      if (MODE >= kFc1Q && cur.t.vrows < cur.t.rows) zero_pads<false>(cur.t, acc);
+      finish_tile<MODE, false>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, 0, acc, elo, ehi, rslots);
     } else {
       f32x16 acc[2][2];
-      nbp = mainloop_ring<true>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
+      nbp = mainloop_ring<true, P_MN>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
                                 nn, acc);
-      if (MODE == kFc1Q && cur.t.vrows < cur.t.rows) zero_pads<true>(cur.t, acc);
-      finish_tile<MODE, true>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, 0, acc, elo, ehi);
+      if (MODE >= kFc1Q && cur.t.vrows < cur.t.rows) zero_pads<true>(cur.t, acc);
+      finish_tile<MODE, true>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, 0, acc, elo, ehi, rslots);
     }
     const int n = cur.ke - cur.kb;
     p.a ^= n & 1;
@@ -2713,9 +2722,13 @@ hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offs
                static_cast<uint8_t*>(const_cast<void*>(q)),
                static_cast<uint8_t*>(const_cast<void*>(qs)), src_row, topk_w, nslots, dots};
   const bf16_t* w = static_cast<const bf16_t*>(w2);
-  hipLaunchKernelGGL((gg_bf16_kernel<kDgradQ, true>), dim3(G), dim3(NTHR), 0, s,
-                     static_cast<const bf16_t*>(dout_perm), sg, E, D, F, mc, w, w, D, ep, ws,
-                     slots, MxScales{});
+  const bf16_t* a = static_cast<const bf16_t*>(dout_perm);
+  if (use_ring(E, m_cap))
+    hipLaunchKernelGGL(gg_ring_kernel<kDgradQ>, dim3(G), dim3(NTHR), 0, s, a, sg, E, D, F, mc, w,
+                       w, ep, ws, slots);
+  else
+    hipLaunchKernelGGL((gg_bf16_kernel<kDgradQ, true>), dim3(G), dim3(NTHR), 0, s, a, sg, E, D, F,
+                       mc, w, w, D, ep, ws, slots, MxScales{});
   if (slots)
     hipLaunchKernelGGL(gg_tail_reduce<kDgradQ>, dim3(4 * G), dim3(256), 0, s, sg, E, D, mc, G,
                        slots, ws, ep, kMinSaved);
