@@ -1870,19 +1870,22 @@ struct RingPos {
 // panel pieces of step s+2 are the last vector-memory instructions it issues in step s,
 // so the wait at the top of step s+1 leaves exactly those 4 in flight. Returns the
 // next tile's bpre.
-template <bool HALF, bool P_MN = false, bool NARROW = false>
+// GUARD as in mainloop (the large backward 478 -> 469 us).
+template <bool HALF, bool P_MN = false, bool NARROW = false, bool GUARD = false>
 __device__ __forceinline__ int mainloop_ring(char* smem, const TileLoads& ld, int kb, int ke,
                                              RingPos p0, bool aprimed, int bpre,
                                              const TileLoads& nxt, bool has_next, int nkb,
-                                             int nn, f32x16 (&acc)[Waves<HALF, NARROW>::blocks][2]) {
+                                             int nn, f32x16 (&acc)[Waves<HALF, NARROW>::blocks][2],
+                                             int vrows = BM) {
   constexpr int WM = Waves<HALF, NARROW>::blocks;
   constexpr int WN = 2;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
-  const int wave = tid >> 6;
+  const int wave = GUARD ? __builtin_amdgcn_readfirstlane(tid >> 6) : tid >> 6;
   const int arow0 = Waves<HALF, NARROW>::row0(wave);
   const int prow0 = Waves<HALF, NARROW>::col(wave) * 64;
   const uint32_t lds0 = lds_addr(smem) + wave * 1024;
+  const int nmb = GUARD ? max(0, min(WM, (vrows - arow0 + 31) >> 5)) : WM;
   const uint32_t ldsb = lds0 + 2 * A_BYTES - A_BYTES;   // issue_loads adds A_BYTES for the panel
 
 #pragma unroll
@@ -1935,11 +1938,13 @@ __device__ __forceinline__ int mainloop_ring(char* smem, const TileLoads& ld, in
       if (ks == 1 && dob) issue_b(bnext);
       if (ks + 1 < BK / 16) frag(ks + 1, (ks + 1) & 1);
 #pragma unroll
-      for (int mb = 0; mb < WM; ++mb)
+      for (int mb = 0; mb < WM; ++mb) {
+        if (GUARD && mb >= nmb) continue;
 #pragma unroll
         for (int nb = 0; nb < WN; ++nb)
           acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[ks & 1][nb], af[ks & 1][mb],
                                                                 acc[mb][nb], 0, 0, 0);
+      }
     }
     tail4 = dob && bnext == s + 2;
     if (dob) ++bnext;
@@ -2044,14 +2049,22 @@ __global__ __launch_bounds__(NTHR, 1) void gg_ring_kernel(
     }
     if (cur.t.rows > BM / 2) {
       f32x16 acc[4][2];
-      nbp = mainloop_ring<false, P_MN>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
-                                 nn, acc);
+      if (MODE >= kFc1Q && cur.t.vrows < cur.t.rows)
+        nbp = mainloop_ring<false, P_MN, false, true>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl,
+                                                     has_next, nw.kb, nn, acc, cur.t.vrows);
+      else
+        nbp = mainloop_ring<false, P_MN>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next,
+                                        nw.kb, nn, acc);
       if (MODE >= kFc1Q && cur.t.vrows < cur.t.rows) zero_pads<false>(cur.t, acc);
       finish_tile<MODE, false>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, 0, acc, elo, ehi, rslots);
     } else {
       f32x16 acc[2][2];
-      nbp = mainloop_ring<true, P_MN>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next, nw.kb,
-                                nn, acc);
+      if (MODE >= kFc1Q && cur.t.vrows < cur.t.rows)
+        nbp = mainloop_ring<true, P_MN, false, true>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl,
+                                                     has_next, nw.kb, nn, acc, cur.t.vrows);
+      else
+        nbp = mainloop_ring<true, P_MN>(smem, ld, cur.kb, cur.ke, p, aprimed, bpre, nl, has_next,
+                                        nw.kb, nn, acc);
       if (MODE >= kFc1Q && cur.t.vrows < cur.t.rows) zero_pads<true>(cur.t, acc);
       finish_tile<MODE, true>(smem, cur.t, ep, cur.kb, cur.ke, cur.part, 0, acc, elo, ehi, rslots);
     }
