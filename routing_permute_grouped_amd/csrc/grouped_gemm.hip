@@ -184,11 +184,11 @@ __device__ __forceinline__ void run_to_groups(uint32_t (&w)[4]) {
 // stored and rows past its tokens read as zeros with no branch around an access. (With the
 // accesses under branches the compiler kept each block's loads behind the block before:
 // 230 us of epilogue in 569 us, 138 of them waiting for the codes.) The whole offset is
-// the lane's, the scalar one 0, for two reasons: the hardware compares the lane's offset with
-// the size less the scalar offset, without a sign, so that a scalar offset past the size would
-// let every lane through; and a 16-byte store with a scalar offset register was seen to take
+// the lane's, the scalar one 0: a 16-byte store with a scalar offset register was seen to take
 // its data's successor when the next instruction wrote the register (lanes 12-15 and 28-31
-// stored it now and then): the compiler puts a wait between the two only without one.
+// stored it now and then): the compiler puts a wait between the two only without one. (The
+// range check itself is safe with either: lanes whose two offsets together reach the size are
+// dropped, a scalar offset past the size drops all of them, and so does a size of 0.)
 typedef __amdgpu_buffer_rsrc_t rows_t;
 __device__ __forceinline__ rows_t tile_rows(const void* p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
