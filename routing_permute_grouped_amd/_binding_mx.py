@@ -71,8 +71,28 @@ def _run(name: str, stream, *args) -> None:
         B._check(name, fn(*c, _raw_stream(dev) if stream is None else B._stream(stream)))
 
 
-def _scale_bytes(rows: int, C: int) -> int:
-    return rows * (C // 32)
+def _scales(t: Optional[torch.Tensor], name: str, rows: int, C: int, layout: int) -> None:
+    """t (if given) holds the scales of ``rows`` rows of C values in ``layout``. Both layouts have
+    as many bytes, so the shape tells them apart: scale rows [..., C/32]; k-step words
+    [C/128, rows, 4] (the rows' axis may be split), over exactly these rows, which are the
+    words' stride. A flat buffer has no such shape and is taken as it is; of one row or one step
+    both layouts are the same bytes."""
+    if t is None:
+        return
+    words = layout == B.MOE_MX_KSTEPS
+    if words and t.shape == (C // 128, rows, 4) and t.dtype == torch.uint8:
+        return
+    n = rows * (C // 32)
+    B._numel(t, name, n, torch.uint8)
+    if t.dim() < 2 or C % (128 if words else 32) or (rows == 1 and t.numel() == n):
+        return
+    if words and C > 128:
+        ok = t.shape[0] == C // 128 and t.shape[-1] == 4 and t.numel() == n
+    else:
+        ok = t.shape[-1] == C // 32
+    if not ok:
+        kind = f"k-step words {(C // 128, rows, 4)}" if words else f"scale rows [{rows}, {C // 32}]"
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {kind}")
 
 
 def _block_rows(codes: torch.Tensor, name: str, per: int) -> Tuple[int, int]:
@@ -105,7 +125,7 @@ def moe_quantize_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
         scales = x.new_empty((C // 128, R, 4) if layout == B.MOE_MX_KSTEPS else (*lead, C // 32),
                              dtype=torch.uint8)
     else:
-        B._numel(scales, "scales", _scale_bytes(R, C), torch.uint8)
+        _scales(scales, "scales", R, C, layout)
     _run("moe_quantize_mxfp4", stream, B._dt(x), ("x", x), R, C, ("q", q), ("scales", scales),
          layout)
     return q, scales
@@ -113,7 +133,7 @@ def moe_quantize_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
 
 def _dequantize(name: str, per: int, q, scales, out, layout, dtype, stream) -> torch.Tensor:
     R, C = _block_rows(q, "q", per)
-    B._numel(scales, "scales", _scale_bytes(R, C), torch.uint8)
+    _scales(scales, "scales", R, C, layout)
     if out is None:
         if dtype not in B._LAYER_DTYPES:
             raise TypeError(f"dtype {dtype}, expected float32 or bfloat16")
@@ -149,7 +169,7 @@ def moe_permute_mxfp4(xq: torch.Tensor, xs: torch.Tensor, topk_idx: torch.Tensor
     metadata. Buffers given in ``out`` are reused."""
     B._dims(xq, "xq", 2)
     T, D = _block_rows(xq, "xq", 1)
-    B._numel(xs, "xs", _scale_bytes(T, D), torch.uint8)
+    _scales(xs, "xs", T, D, B.MOE_MX_ROWS)
     k = B._check_idx(topk_idx, T)
     dev = xq.device
     if m_cap is None:
@@ -158,7 +178,7 @@ def moe_permute_mxfp4(xq: torch.Tensor, xs: torch.Tensor, topk_idx: torch.Tensor
             raise ValueError(f"no capacity for T={T}, k={k}, E={E}, m_tile={m_tile}")
     o = dict(out or {})
     B._rows(o.get("xq_perm"), "xq_perm", m_cap, D // 2, torch.uint8)
-    B._numel(o.get("xs_perm"), "xs_perm", (D // 128) * m_cap * 4, torch.uint8)
+    _scales(o.get("xs_perm"), "xs_perm", m_cap, D, B.MOE_MX_KSTEPS)
     B._check_layout_out(o, T, k, E, m_cap, m_tile)
     ws = max(4, B.moe_permute_workspace_bytes(T, k, E))
     B._nbytes(o.get("workspace"), "workspace", ws)
@@ -191,13 +211,13 @@ def _mx4_weight(q: torch.Tensor, s: torch.Tensor, name: str, shape=None) -> Tupl
     if shape is not None and (E, N, K) != tuple(shape):
         raise ValueError(f"{name}q: shape {tuple(q.shape)}, expected "
                          f"{(shape[0], shape[1], shape[2] // 2)}")
-    B._numel(s, name + "s", (K // 128) * E * N * 4, torch.uint8)
+    _scales(s, name + "s", E * N, K, B.MOE_MX_KSTEPS)
     return E, N, K
 
 
 def _mx4_rows(q: torch.Tensor, s: torch.Tensor, name: str, m_cap: int, K: int) -> None:
     B._rows(q, name + "q", m_cap, K // 2, torch.uint8)
-    B._numel(s, name + "s", (K // 128) * m_cap * 4, torch.uint8)
+    _scales(s, name + "s", m_cap, K, B.MOE_MX_KSTEPS)
 
 
 def _wsz(ws: Optional[torch.Tensor]) -> int:
