@@ -1,7 +1,8 @@
 """ctypes binding of the calls include/moe_mx.h declares: 4-bit quantisation and products,
 8-bit checkpoints of fc1's pre-activations. Argument marshalling only, in the manner of
 ``_binding``; each call runs on the device of its first tensor (all others must be there)
-and, without ``stream``, on that device's current stream.
+and, without ``stream``, on that device's current stream. With ``stream``, what the caller does
+not give is allocated there, so the call is ordered by that stream alone.
 """
 from __future__ import annotations
 
@@ -71,6 +72,21 @@ def _run(name: str, stream, *args) -> None:
         B._check(name, fn(*c, _raw_stream(dev) if stream is None else B._stream(stream)))
 
 
+def _new(stream, dev: torch.device, shape, dtype: torch.dtype) -> torch.Tensor:
+    """A buffer of the call's own, from the memory of the stream that the call runs on: a block of
+    the current stream's may come from a tensor that work queued there still uses, and nothing
+    orders ``stream`` behind that work. What the current stream does with the buffer later
+    keeps it from reuse."""
+    if stream is None or dev.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(B._stream(stream), device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def _scales(t: Optional[torch.Tensor], name: str, rows: int, C: int, layout: int) -> None:
     """t (if given) holds the scales of ``rows`` rows of C values in ``layout``. Both layouts have
     as many bytes, so the shape tells them apart: scale rows [..., C/32]; k-step words
@@ -118,12 +134,12 @@ def moe_quantize_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     *lead, C = x.shape
     R = n // C
     if q is None:
-        q = x.new_empty((*lead, C // 2), dtype=torch.uint8)
+        q = _new(stream, x.device, (*lead, C // 2), torch.uint8)
     else:
         B._numel(q, "q", n // 2, torch.uint8)
     if scales is None:
-        scales = x.new_empty((C // 128, R, 4) if layout == B.MOE_MX_KSTEPS else (*lead, C // 32),
-                             dtype=torch.uint8)
+        scales = _new(stream, x.device, (C // 128, R, 4) if layout == B.MOE_MX_KSTEPS
+                      else (*lead, C // 32), torch.uint8)
     else:
         _scales(scales, "scales", R, C, layout)
     _run("moe_quantize_mxfp4", stream, B._dt(x), ("x", x), R, C, ("q", q), ("scales", scales),
@@ -137,7 +153,7 @@ def _dequantize(name: str, per: int, q, scales, out, layout, dtype, stream) -> t
     if out is None:
         if dtype not in B._LAYER_DTYPES:
             raise TypeError(f"dtype {dtype}, expected float32 or bfloat16")
-        out = q.new_empty((*q.shape[:-1], C), dtype=dtype)
+        out = _new(stream, q.device, (*q.shape[:-1], C), dtype)
     else:
         B._layer_dtype(out, "out")
         B._numel(out, "out", R * C)
@@ -182,16 +198,13 @@ def moe_permute_mxfp4(xq: torch.Tensor, xs: torch.Tensor, topk_idx: torch.Tensor
     B._check_layout_out(o, T, k, E, m_cap, m_tile)
     ws = max(4, B.moe_permute_workspace_bytes(T, k, E))
     B._nbytes(o.get("workspace"), "workspace", ws)
-    i32 = dict(dtype=torch.int32, device=dev)
-    o.setdefault("xq_perm", torch.empty((m_cap, D // 2), dtype=torch.uint8, device=dev))
-    o.setdefault("xs_perm", torch.empty((D // 128, m_cap, 4), dtype=torch.uint8, device=dev))
-    o.setdefault("counts", torch.empty(E, **i32))
-    o.setdefault("offsets", torch.empty(E + 1, **i32))
-    o.setdefault("dst_row", torch.empty((T, k), **i32))
-    o.setdefault("src_row", torch.empty(m_cap, **i32))
-    o.setdefault("tile_expert", torch.empty(m_cap // m_tile, **i32))
-    o.setdefault("dev_err", torch.empty(1, **i32))
-    o.setdefault("workspace", torch.empty(ws, dtype=torch.uint8, device=dev))
+    u8, i32 = torch.uint8, torch.int32
+    for n, shape, dt in (("xq_perm", (m_cap, D // 2), u8), ("xs_perm", (D // 128, m_cap, 4), u8),
+                         ("counts", E, i32), ("offsets", E + 1, i32), ("dst_row", (T, k), i32),
+                         ("src_row", m_cap, i32), ("tile_expert", m_cap // m_tile, i32),
+                         ("dev_err", 1, i32), ("workspace", ws, u8)):
+        if n not in o:
+            o[n] = _new(stream, dev, shape, dt)
     wsb = o["workspace"].numel() * o["workspace"].element_size()
     _run("moe_permute_mxfp4", stream, ("xq", xq), ("xs", xs), ("topk_idx", topk_idx), T, D, E, k,
          m_tile, m_cap, ("xq_perm", o["xq_perm"]), ("xs_perm", o["xs_perm"]),
@@ -242,7 +255,7 @@ def moe_grouped_fc1_swiglu_mxfp4(xq_perm: torch.Tensor, xs_perm: torch.Tensor,
     B._numel(counts, "counts", E, torch.int32)
     B._rows(h, "h", m_cap, F, torch.bfloat16)
     if h is None:
-        h = torch.empty((m_cap, F), dtype=torch.bfloat16, device=xq_perm.device)
+        h = _new(stream, xq_perm.device, (m_cap, F), torch.bfloat16)
     _run("moe_grouped_fc1_swiglu_mxfp4", stream, ("xq_perm", xq_perm), ("xs_perm", xs_perm),
          ("offsets", offsets), ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile,
          m_cap, ("w1q", w1q), ("w1s", w1s), ("w3q", w3q), ("w3s", w3s), ("h", h),
@@ -266,7 +279,7 @@ def moe_grouped_fc2_mxfp4(hq: torch.Tensor, hs: torch.Tensor, offsets: torch.Ten
     B._numel(counts, "counts", E, torch.int32)
     B._rows(y_perm, "y_perm", m_cap, D, torch.bfloat16)
     if y_perm is None:
-        y_perm = torch.empty((m_cap, D), dtype=torch.bfloat16, device=hq.device)
+        y_perm = _new(stream, hq.device, (m_cap, D), torch.bfloat16)
     _run("moe_grouped_fc2_mxfp4", stream, ("hq", hq), ("hs", hs), ("offsets", offsets),
          ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w2q", w2q),
          ("w2s", w2s), ("y_perm", y_perm), ("workspace", workspace), _wsz(workspace))
@@ -290,9 +303,9 @@ def moe_grouped_swiglu_masked_mxfp4(x_masked: torch.Tensor, counts: torch.Tensor
     B._rows(y, "y", E * cap, D, torch.bfloat16)
     dev = x_masked.device
     if h is None:
-        h = torch.empty((E * cap, F), dtype=torch.bfloat16, device=dev)
+        h = _new(stream, dev, (E * cap, F), torch.bfloat16)
     if y is None:
-        y = torch.empty((E * cap, D), dtype=torch.bfloat16, device=dev)
+        y = _new(stream, dev, (E * cap, D), torch.bfloat16)
     _run("moe_grouped_swiglu_masked_mxfp4", stream, ("x_masked", x_masked), ("counts", counts), E,
          D, F, cap, ("w1q", w1q), ("w1s", w1s), ("w3q", w3q), ("w3s", w3s), ("w2q", w2q),
          ("w2s", w2s), ("h", h), ("y", y))
@@ -324,11 +337,11 @@ def moe_grouped_fc1_swiglu_ckpt8(x_perm: torch.Tensor, offsets: torch.Tensor,
     B._rows(ab_scales, "ab_scales", m_cap, F // 16, torch.uint8)
     dev = x_perm.device
     if h is None:
-        h = torch.empty((m_cap, F), dtype=torch.bfloat16, device=dev)
+        h = _new(stream, dev, (m_cap, F), torch.bfloat16)
     if ab_codes is None:
-        ab_codes = torch.empty((m_cap, 2 * F), dtype=torch.uint8, device=dev)
+        ab_codes = _new(stream, dev, (m_cap, 2 * F), torch.uint8)
     if ab_scales is None:
-        ab_scales = torch.empty((m_cap, F // 16), dtype=torch.uint8, device=dev)
+        ab_scales = _new(stream, dev, (m_cap, F // 16), torch.uint8)
     _run("moe_grouped_fc1_swiglu_ckpt8", stream, ("x_perm", x_perm), ("offsets", offsets),
          ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w1", w1),
          ("w3", w3), ("h", h), ("ab_codes", ab_codes), ("ab_scales", ab_scales),
@@ -389,18 +402,16 @@ def moe_grouped_dgrad_swiglu_ckpt8(dout_perm: torch.Tensor, offsets: torch.Tenso
     elif dtopk_w is not None:
         raise ValueError("dtopk_w needs topk_w")
     if dab is None:
-        dab = torch.empty((m_cap, 2 * F), dtype=torch.bfloat16, device=dev)
+        dab = _new(stream, dev, (m_cap, 2 * F), torch.bfloat16)
     if hw is None:
-        hw = torch.empty((m_cap, F), dtype=torch.bfloat16, device=dev)
+        hw = _new(stream, dev, (m_cap, F), torch.bfloat16)
     if topk_w is None:
         src_row = dst_row = scratch = None
     else:
         if dtopk_w is None:
-            dtopk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+            dtopk_w = _new(stream, dev, (T, k), torch.float32)
         if scratch is None:
-            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-            if stream is not None:   # freed on return, but that stream still uses it
-                scratch.record_stream(torch.cuda.ExternalStream(B._stream(stream), device=dev))
+            scratch = _new(stream, dev, need, torch.uint8)
     _run("moe_grouped_dgrad_swiglu_ckpt8", stream, ("dout_perm", dout_perm), ("offsets", offsets),
          ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w2", w2),
          ("ab_codes", ab_codes), ("ab_scales", ab_scales), ("src_row", src_row),
