@@ -2666,20 +2666,23 @@ hipError_t launch_grouped_fc1_mx(const void* xq_perm, const void* xs_perm,
 }
 
 // Each slot's sum of its row's partial sums, eight lanes a slot, in a fixed order; 0 for slots
-// without a row. (A row's sums side by side, 49152 slots of 22: 9.4 -> 6.0 us.)
+// without a row. The workgroups stride over the slots: one for every 32 would pass the 2^32
+// threads of a launch from 2^29 slots. (A row's sums side by side, 49152 slots of 22: 9.4 -> 6.0 us.)
 __global__ __launch_bounds__(256) void row_dot_kernel(const int32_t* __restrict__ dst_row,
                                                       const float* __restrict__ dots, int nslots,
                                                       int m_cap, int parts,
                                                       float* __restrict__ out) {
-  const int64_t s = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 3;
   const int l = threadIdx.x & 7;
-  const int r = s < nslots ? dst_row[s] : -1;
-  float sum = 0.0f;
-  if (r >= 0 && r < m_cap)
-    for (int p = l; p < parts; p += 8) sum += dots[(size_t)r * parts + p];
+  for (int64_t s0 = (int64_t)blockIdx.x * 32; s0 < nslots; s0 += (int64_t)gridDim.x * 32) {
+    const int64_t s = s0 + (threadIdx.x >> 3);
+    const int r = s < nslots ? dst_row[s] : -1;
+    float sum = 0.0f;
+    if (r >= 0 && r < m_cap)
+      for (int p = l; p < parts; p += 8) sum += dots[(size_t)r * parts + p];
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor(sum, d);
-  if (l == 0 && s < nslots) out[s] = sum;
+    for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor(sum, d);
+    if (l == 0 && s < nslots) out[s] = sum;
+  }
 }
 
 size_t ckpt8_scratch_bytes(int F, int64_t m_cap) {
@@ -2746,8 +2749,9 @@ hipError_t launch_grouped_dgrad_ckpt8(const void* dout_perm, const int32_t* offs
     hipLaunchKernelGGL(gg_tail_reduce<kDgradQ>, dim3(4 * G), dim3(256), 0, s, sg, E, D, mc, G,
                        slots, ws, ep, kMinSaved);
   if (dtopk_w)
-    hipLaunchKernelGGL(row_dot_kernel, dim3((unsigned)(((int64_t)nslots + 31) / 32)), dim3(256), 0, s, dst_row, dots,
-                       nslots, mc, F / 64, dtopk_w);
+    hipLaunchKernelGGL(row_dot_kernel,
+                       dim3((unsigned)std::min<int64_t>(64 * G, ((int64_t)nslots + 31) / 32)),
+                       dim3(256), 0, s, dst_row, dots, nslots, mc, F / 64, dtopk_w);
   return hipGetLastError();
 }
 
