@@ -2,6 +2,9 @@
 // against expert weights held as E2M1 codes (two a byte, the even k in the low half) with
 // one E8M0 scale per 32 values, in k-step words. Per expert e and valid row:
 //   h = silu(x w1^T) * (x w3^T) rounded to bf16, y = h w2^T, float32 sums.
+// h is rounded once to bf16, its type as an output and as an operand of fc2's matrix
+// instruction, as in the masked path with bf16 weights (y is then off by about 2.4e-3 of its size,
+// with a float32 h by 1.7e-3).
 //
 // Bound by the stream of the active experts' weights, 17/32 byte a value, a quarter of the
 // bf16 stream; per weight byte there is four times the work on the rows. Hence
@@ -18,8 +21,9 @@
 //     values, exactly (one fraction bit, and a power of two), and v_mfma_f32_16x16x32_bf16
 //     multiplies;
 //   * rows come through LDS, KS chunks at a time, double-buffered through registers, one
-//     barrier per KS chunks; weights run PD groups of KS chunks ahead in registers. All loads
-//     are ordinary ones, so every wait is the compiler's own;
+//     barrier per KS chunks. A group's weights lie in registers and are refilled with the next
+//     group's once they are multiplied. All loads are ordinary ones, so every wait is the
+//     compiler's own;
 //   * four workgroups a CU hide the latency; deeper prefetch at three or two was slower (64
 //     experts of D = 2048, F = 1408, one row each: 57 us, at two workgroups and 16 chunks
 //     ahead 94), and so was splitting k over all four waves (100 us);
@@ -101,10 +105,10 @@ __device__ __forceinline__ void spread(uint32_t word, int g, float (&scale)[KS])
     scale[i] = __uint_as_float(__builtin_amdgcn_ubfe(w[i], 8 * g, 8) << 23);
 }
 
-// NB: row blocks of 16 of the item's rows; KS: 128-value chunks per LDS buffer; PD: groups of
-// chunks in flight; KW: waves that share 16 columns, each taking every KW-th chunk (the item is
-// 64 / KW columns, and their sums are added in wave order). cols: the item's first column.
-template <bool FC1, int NB, int KS, int PD, int KW>
+// NB: row blocks of 16 of the item's rows; KS: 128-value chunks per LDS buffer, and of weights in
+// flight; KW: waves that share 16 columns, each taking every KW-th chunk (the item is 64 / KW
+// columns, and their sums are added in wave order). cols: the item's first column.
+template <bool FC1, int NB, int KS, int KW>
 __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X, int cols, int e,
                                           int r0, int rows, int K, int N, int E,
                                           const Mx4Weights& wt, bf16_t* __restrict__ out) {
@@ -129,19 +133,19 @@ __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X
   const uint8_t* wrow[2] = {wt.q1 + row * (K / 2) + 16 * g, wt.q2 + row * (K / 2) + 16 * g};
   const uint32_t* srow[2] = {wt.s1 + row, wt.s2 + row};
   const size_t sstep = (size_t)E * N;
-  u32x4 wr[PD][NW][KC];
-  uint32_t sr[PD][NW];
+  u32x4 wr[NW][KC];
+  uint32_t sr[NW];
   // past the last chunk of a group that K ends in, the last one again; its rows are zeros there
-  auto wload = [&](int slot, int gr) {
+  auto wload = [&](int gr) {
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int c = min(gr * KS + i * KW + kw, nch - 1);
 #pragma unroll
-      for (int w = 0; w < NW; ++w) wr[slot][w][i] = ld16(wrow[w] + (size_t)c * 64);
+      for (int w = 0; w < NW; ++w) wr[w][i] = ld16(wrow[w] + (size_t)c * 64);
     }
 #pragma unroll
     for (int w = 0; w < NW; ++w)
-      sr[slot][w] = srow[w][min(gr * KS + g % KC * KW + kw, nch - 1) * sstep];
+      sr[w] = srow[w][min(gr * KS + g % KC * KW + kw, nch - 1) * sstep];
   };
 
   // unit q of a group: row q / (16*KS), 16-byte unit q % (16*KS) of the row's group
@@ -172,18 +176,18 @@ __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[w][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto compute = [&](int buf, int slot) {
+  auto compute = [&](int buf) {
     const char* xb = xs + buf * (XBYTES / 2);
     float scale[NW][KC];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) spread<KC>(sr[slot][w], g, scale[w]);
+    for (int w = 0; w < NW; ++w) spread<KC>(sr[w], g, scale[w]);
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         bf16x8 wf[NW];
 #pragma unroll
-        for (int w = 0; w < NW; ++w) wf[w] = dequant8(wr[slot][w][i][s], scale[w][i]);
+        for (int w = 0; w < NW; ++w) wf[w] = dequant8(wr[w][i][s], scale[w][i]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const int r = 16 * b + fr;
@@ -198,26 +202,18 @@ __device__ __forceinline__ void dec4_body(char* xs, const bf16_t* __restrict__ X
   };
 
   xload(0);
-#pragma unroll
-  for (int p = 0; p < PD; ++p)
-    if (p < ngr) wload(p, p);
+  wload(0);
   lds_barrier();   // the item before is done with the buffers
   xstore(0);
   xload(1);
   lds_barrier();
-  for (int g0 = 0; g0 < ngr; g0 += PD) {
-#pragma unroll
-    for (int j = 0; j < PD; ++j) {
-      const int gr = g0 + j;
-      if (gr < ngr) {
-        compute(gr & 1, j);
-        // the other buffer's readers passed the barrier that ended the step before
-        xstore((gr + 1) & 1);
-        xload(gr + 2);
-        if (gr + PD < ngr) wload(j, gr + PD);
-        lds_barrier();
-      }
-    }
+  for (int gr = 0; gr < ngr; ++gr) {
+    compute(gr & 1);
+    // the other buffer's readers passed the barrier that ended the step before
+    xstore((gr + 1) & 1);
+    xload(gr + 2);
+    if (gr + 1 < ngr) wload(gr + 1);
+    lds_barrier();
   }
 
   if (KW > 1) {   // every wave is past its last read of the row buffers
@@ -328,17 +324,17 @@ __global__ __launch_bounds__(DW * 64, 4) void dec4_kernel(const bf16_t* __restri
     const int first = in / width * GROUP, cols = (base + in % width) * width0;
     const int rows = min(n - first, GROUP), r0 = e * cap + first;
     if (rows <= 16 && halve)
-      dec4_body<FC1, 1, 4, 1, 2>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 1, 4, 2>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
     else if (rows <= 16)
-      dec4_body<FC1, 1, 4, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 1, 4, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
     else if (rows <= 32 && halve)
-      dec4_body<FC1, 2, 2, 1, 2>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 2, 2, 2>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
     else if (rows <= 32)
-      dec4_body<FC1, 2, 2, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 2, 2, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
     else if (rows <= 48)
-      dec4_body<FC1, 3, 1, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 3, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
     else
-      dec4_body<FC1, 4, 1, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
+      dec4_body<FC1, 4, 1, 1>(xs, X, cols, e, r0, rows, K, N, E, wt, out);
   }
 }
 
