@@ -117,8 +117,9 @@ moe_status_t moe_grouped_swiglu_masked_mxfp4(const void* x_masked, const int32_t
 /*
  * moe_grouped_fc1_swiglu_ckpt8 - moe_grouped_fc1_swiglu (bf16) that keeps the
  * pre-activations for the backward as MXFP8 in place of bf16:
- *   -> h [m_cap,F] bf16, bit for bit moe_grouped_fc1_swiglu's without a workspace (with one
- *                    the two calls may cut different tiles over k: another order of sums)
+ *   -> h [m_cap,F] bf16, bit for bit what moe_grouped_fc1_swiglu with ab gives, both without a
+ *                    workspace (with one the two calls may cut different tiles over k:
+ *                    another order of sums; without ab a decode-sized call sums otherwise too)
  *      ab_codes [m_cap,2F] e4m3 codes of [a | b], ab_scales [m_cap,2F/32] bytes
  *                    (4-byte aligned)
  * Blocks are 32 consecutive columns of a or of b, quantised from the float32 sums. Pad rows

@@ -734,8 +734,10 @@ __device__ __forceinline__ void fc1q_epilogue(const Tile& t, const Epi& ep,
 // ahead. The products of a row's 64 columns are summed in the lane, then over the two lane
 // halves. About 100 cycles of vector arithmetic an element of the wave, 32 of them in the
 // sigmoid's exponential and reciprocal: 11 us of a full tile, against 60 for its 32 k-steps (8192
-// tokens top-6 over 64 experts, D = 2048, F = 1408: 478 us, 345 without the epilogue). Stores of
-// whole 64-byte pieces gained 3% before the lane swaps they take, non-temporal ones lost 13%.
+// tokens top-6 over 64 experts, D = 2048, F = 1408: 473 us, 332 without the epilogue; the rest of
+// the difference is its loads and stores, which the next tile's first step waits for). On the
+// two-stage kernel stores of whole 64-byte pieces gained 3% before the lane swaps they take and
+// non-temporal ones lost 13%.
 //
 // Slots: the slots of the wave's rows, one or two a lane, asked for before the main loop so
 // that only the weights' own load is left to wait for here.
@@ -1506,13 +1508,16 @@ __device__ Tile decode_item(const Sched& sc, int E, int n_nt, int cols, int w, i
 //
 // min_saved: a tile is cut only if that saves at least so many k-steps of the round. The
 // 4-bit products and the checkpoint's two GEMMs ask for 20: writing, reading and adding the
-// shares costs 7 to 15 us, and a reduction that finds nothing to add 4. (Cut against uncut in
-// halved row blocks, 200 tokens of one expert, 2048 columns: 4-bit fc2, F = 4096 (14 steps
-// saved) 27.4 against 25.3 us, F = 8192 (28) 30.4 against 40.6.) Few tiles of the checkpoint's
-// GEMMs are better made smaller (plan_rows) up to 50 steps saved: fc1 of that expert, D = 2048
-// (28) 36.4 against 29.3 us, D = 4096 (56) 42.8 against 46.1; the backward, 1500 tokens top-2
-// over 8 experts, F = 1024, D = 4096 (48) 61.7 against 54.0; 389 tokens, F = 1088 (53) 42.6
-// against 50.4.
+// shares costs about as much, 7 to 15 us in calls of one round and up to 30 where the tail is
+// long (the reduction alone takes 26 of the large backward), and a reduction that finds nothing
+// to add 4 to 8. (Cut against whole: the backward, 8192 tokens top-6 over 64 experts, F = 1408,
+// D = 1536 (16 steps saved) 392 against 387 us, D = 2048 (21) 445 against 445, D = 4096 (42) 731
+// against 752; 4-bit fc1, 2025 tokens top-8 over 32 experts, F = 512, D = 7168 (18) 105 against
+// 103, D = 10240 (26) 137 against 148; 4-bit fc2, 8192 tokens top-6 over 64 experts, D = 1408,
+// F = 7168 (18) 313 against 315.) Few tiles of the checkpoint's GEMMs are better made smaller
+// (plan_rows) up to 50 steps saved: fc1, 200 tokens of one expert, F = 2048, D = 2048 (28) 34
+// against 27 us, D = 4096 (56) 40 against 45; the backward, 1500 tokens top-2 over 8 experts,
+// F = 1024, D = 4096 (48) 75 against 68; 389 tokens, F = 1088 (53) 55 against 62.
 constexpr int kMinSaved = 20;
 
 struct Split {
@@ -1551,12 +1556,12 @@ __device__ Split split_plan(int total, int G, int slots, int nk, int min_saved,
 // The 4-bit products and the checkpoint's two GEMMs halve the row blocks where whole tiles
 // would leave half of the workgroups idle, unless a cut over k puts at least three of them on
 // a tile. (Halves against whole tiles, 1500 tokens top-2 over 8 experts, F = 1024: fc1 with the
-// checkpoint, D = 1024 29.9 against 39.0 us; its backward, D = 512 29.8 against 39.7; 4-bit
-// fc1, D = 4096 28.0 against 36.7. Halves against a cut in two: 4-bit fc1, D = 8192 46.1 against
-// 57.1 us.) Where that still leaves half of them idle, the checkpoint's GEMMs halve the columns
-// as well: their epilogues are long, and the panel's unused half is loaded only to keep the
-// loads as they are (389 tokens top-2 over 8 experts, D = 512, F = 1088: fc1 21.5 -> 17.1 us,
-// the backward 29.9 -> 24.9, on the ring then 20.9).
+// checkpoint, D = 1024 27 against 37 us; its backward, D = 512 22.6 against 39.5; 4-bit fc1,
+// D = 4096 27.6 against 36. Halves against a cut in two: 4-bit fc1, D = 10240 69 us, 77 with a
+// reduction that finds nothing, against 77.) Where that still leaves half of them idle, the
+// checkpoint's GEMMs halve the columns as well: their epilogues are long, and the panel's unused
+// half is loaded only to keep the loads as they are (389 tokens top-2 over 8 experts, D = 512, F =
+// 1088: fc1 17.7 -> 13.8 us, the backward 26.1 -> 20.6).
 __device__ __forceinline__ bool may_halve(const Split& sp, int total, int G) {
   return 2 * total <= G && sp.S <= 2;
 }
