@@ -59,20 +59,20 @@ def gemm_source_sha16() -> str:
 # kind: fc1 (forward), wgrad_fc1 (backward), fp8_fc1 (FP8 payload), masked (decode).
 TRAFFIC = {
     "fc1": {
-        "dense8_bf16": (4316417075, "ec23b0769012bcba"),
-        "etp_shard32_bf16": (1034965483, "ec23b0769012bcba"),
-        "fine64_shared2_bf16": (2384506166, "ec23b0769012bcba"),
-        "skew32_zipf_bf16": (5397533361, "ec23b0769012bcba"),
+        "dense8_bf16": (4316874882, "e7bc0b774ba4aa69"),
+        "etp_shard32_bf16": (1034805176, "e7bc0b774ba4aa69"),
+        "fine64_shared2_bf16": (2354090882, "e7bc0b774ba4aa69"),
+        "skew32_zipf_bf16": (5258778240, "e7bc0b774ba4aa69"),
     },
     "wgrad_fc1": {
-        "dense8_bf16": (8144705579, "ec23b0769012bcba"),
+        "dense8_bf16": (7985623706, "e7bc0b774ba4aa69"),
     },
     "fp8_fc1": {
-        "dense8_bf16": (2480918277, "ec23b0769012bcba"),
+        "dense8_bf16": (2468839520, "e7bc0b774ba4aa69"),
     },
     "masked": {
-        "decode8_bf16": (2920594913, "ec23b0769012bcba"),
-        "decode64_shared2_bf16": (1167546070, "ec23b0769012bcba"),
+        "decode8_bf16": (2919851244, "e7bc0b774ba4aa69"),
+        "decode64_shared2_bf16": (1167631421, "e7bc0b774ba4aa69"),
     },
 }
 
