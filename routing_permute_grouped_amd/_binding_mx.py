@@ -72,17 +72,18 @@ def _run(name: str, stream, *args) -> None:
         B._check(name, fn(*c, _raw_stream(dev) if stream is None else B._stream(stream)))
 
 
-def _new(stream, dev: torch.device, shape, dtype: torch.dtype) -> torch.Tensor:
-    """A buffer of the call's own, from the memory of the stream that the call runs on: a block of
-    the current stream's may come from a tensor that work queued there still uses, and nothing
-    orders ``stream`` behind that work. What the current stream does with the buffer later
-    keeps it from reuse."""
-    if stream is None or dev.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _new(stream, like: torch.Tensor, shape, dtype: torch.dtype) -> torch.Tensor:
+    """A buffer of the call's own on ``like``'s device, from the memory of the stream that the call
+    runs on: a block of the current stream's may come from a tensor that work queued there
+    still uses, and nothing orders ``stream`` behind that work. What the current stream does
+    with the buffer later keeps it from reuse."""
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
+    dev = like.device
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(B._stream(stream), device=dev)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = like.new_empty(shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream(dev))
     return t
 
@@ -134,11 +135,11 @@ def moe_quantize_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     *lead, C = x.shape
     R = n // C
     if q is None:
-        q = _new(stream, x.device, (*lead, C // 2), torch.uint8)
+        q = _new(stream, x, (*lead, C // 2), torch.uint8)
     else:
         B._numel(q, "q", n // 2, torch.uint8)
     if scales is None:
-        scales = _new(stream, x.device, (C // 128, R, 4) if layout == B.MOE_MX_KSTEPS
+        scales = _new(stream, x, (C // 128, R, 4) if layout == B.MOE_MX_KSTEPS
                       else (*lead, C // 32), torch.uint8)
     else:
         _scales(scales, "scales", R, C, layout)
@@ -153,7 +154,7 @@ def _dequantize(name: str, per: int, q, scales, out, layout, dtype, stream) -> t
     if out is None:
         if dtype not in B._LAYER_DTYPES:
             raise TypeError(f"dtype {dtype}, expected float32 or bfloat16")
-        out = _new(stream, q.device, (*q.shape[:-1], C), dtype)
+        out = _new(stream, q, (*q.shape[:-1], C), dtype)
     else:
         B._layer_dtype(out, "out")
         B._numel(out, "out", R * C)
@@ -187,7 +188,6 @@ def moe_permute_mxfp4(xq: torch.Tensor, xs: torch.Tensor, topk_idx: torch.Tensor
     T, D = _block_rows(xq, "xq", 1)
     _scales(xs, "xs", T, D, B.MOE_MX_ROWS)
     k = B._check_idx(topk_idx, T)
-    dev = xq.device
     if m_cap is None:
         m_cap = B.moe_capacity(T, k, E, m_tile)
         if m_cap < 0:
@@ -204,7 +204,7 @@ def moe_permute_mxfp4(xq: torch.Tensor, xs: torch.Tensor, topk_idx: torch.Tensor
                          ("src_row", m_cap, i32), ("tile_expert", m_cap // m_tile, i32),
                          ("dev_err", 1, i32), ("workspace", ws, u8)):
         if n not in o:
-            o[n] = _new(stream, dev, shape, dt)
+            o[n] = _new(stream, xq, shape, dt)
     wsb = o["workspace"].numel() * o["workspace"].element_size()
     _run("moe_permute_mxfp4", stream, ("xq", xq), ("xs", xs), ("topk_idx", topk_idx), T, D, E, k,
          m_tile, m_cap, ("xq_perm", o["xq_perm"]), ("xs_perm", o["xs_perm"]),
@@ -255,7 +255,7 @@ def moe_grouped_fc1_swiglu_mxfp4(xq_perm: torch.Tensor, xs_perm: torch.Tensor,
     B._numel(counts, "counts", E, torch.int32)
     B._rows(h, "h", m_cap, F, torch.bfloat16)
     if h is None:
-        h = _new(stream, xq_perm.device, (m_cap, F), torch.bfloat16)
+        h = _new(stream, xq_perm, (m_cap, F), torch.bfloat16)
     _run("moe_grouped_fc1_swiglu_mxfp4", stream, ("xq_perm", xq_perm), ("xs_perm", xs_perm),
          ("offsets", offsets), ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile,
          m_cap, ("w1q", w1q), ("w1s", w1s), ("w3q", w3q), ("w3s", w3s), ("h", h),
@@ -279,7 +279,7 @@ def moe_grouped_fc2_mxfp4(hq: torch.Tensor, hs: torch.Tensor, offsets: torch.Ten
     B._numel(counts, "counts", E, torch.int32)
     B._rows(y_perm, "y_perm", m_cap, D, torch.bfloat16)
     if y_perm is None:
-        y_perm = _new(stream, hq.device, (m_cap, D), torch.bfloat16)
+        y_perm = _new(stream, hq, (m_cap, D), torch.bfloat16)
     _run("moe_grouped_fc2_mxfp4", stream, ("hq", hq), ("hs", hs), ("offsets", offsets),
          ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w2q", w2q),
          ("w2s", w2s), ("y_perm", y_perm), ("workspace", workspace), _wsz(workspace))
@@ -301,11 +301,10 @@ def moe_grouped_swiglu_masked_mxfp4(x_masked: torch.Tensor, counts: torch.Tensor
     B._numel(counts, "counts", E, torch.int32)
     B._rows(h, "h", E * cap, F, torch.bfloat16)
     B._rows(y, "y", E * cap, D, torch.bfloat16)
-    dev = x_masked.device
     if h is None:
-        h = _new(stream, dev, (E * cap, F), torch.bfloat16)
+        h = _new(stream, x_masked, (E * cap, F), torch.bfloat16)
     if y is None:
-        y = _new(stream, dev, (E * cap, D), torch.bfloat16)
+        y = _new(stream, x_masked, (E * cap, D), torch.bfloat16)
     _run("moe_grouped_swiglu_masked_mxfp4", stream, ("x_masked", x_masked), ("counts", counts), E,
          D, F, cap, ("w1q", w1q), ("w1s", w1s), ("w3q", w3q), ("w3s", w3s), ("w2q", w2q),
          ("w2s", w2s), ("h", h), ("y", y))
@@ -335,13 +334,12 @@ def moe_grouped_fc1_swiglu_ckpt8(x_perm: torch.Tensor, offsets: torch.Tensor,
     B._rows(h, "h", m_cap, F, torch.bfloat16)
     B._rows(ab_codes, "ab_codes", m_cap, 2 * F, torch.uint8)
     B._rows(ab_scales, "ab_scales", m_cap, F // 16, torch.uint8)
-    dev = x_perm.device
     if h is None:
-        h = _new(stream, dev, (m_cap, F), torch.bfloat16)
+        h = _new(stream, x_perm, (m_cap, F), torch.bfloat16)
     if ab_codes is None:
-        ab_codes = _new(stream, dev, (m_cap, 2 * F), torch.uint8)
+        ab_codes = _new(stream, x_perm, (m_cap, 2 * F), torch.uint8)
     if ab_scales is None:
-        ab_scales = _new(stream, dev, (m_cap, F // 16), torch.uint8)
+        ab_scales = _new(stream, x_perm, (m_cap, F // 16), torch.uint8)
     _run("moe_grouped_fc1_swiglu_ckpt8", stream, ("x_perm", x_perm), ("offsets", offsets),
          ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w1", w1),
          ("w3", w3), ("h", h), ("ab_codes", ab_codes), ("ab_scales", ab_scales),
@@ -386,7 +384,6 @@ def moe_grouped_dgrad_swiglu_ckpt8(dout_perm: torch.Tensor, offsets: torch.Tenso
     B._rows(ab_scales, "ab_scales", ru, F // 16, torch.uint8)
     B._rows(dab, "dab", m_cap, 2 * F, torch.bfloat16)
     B._rows(hw, "hw", m_cap, F, torch.bfloat16)
-    dev = dout_perm.device
     T = k = need = 0
     if topk_w is not None:
         B._dims(topk_w, "topk_w", 2)
@@ -402,16 +399,16 @@ def moe_grouped_dgrad_swiglu_ckpt8(dout_perm: torch.Tensor, offsets: torch.Tenso
     elif dtopk_w is not None:
         raise ValueError("dtopk_w needs topk_w")
     if dab is None:
-        dab = _new(stream, dev, (m_cap, 2 * F), torch.bfloat16)
+        dab = _new(stream, dout_perm, (m_cap, 2 * F), torch.bfloat16)
     if hw is None:
-        hw = _new(stream, dev, (m_cap, F), torch.bfloat16)
+        hw = _new(stream, dout_perm, (m_cap, F), torch.bfloat16)
     if topk_w is None:
         src_row = dst_row = scratch = None
     else:
         if dtopk_w is None:
-            dtopk_w = _new(stream, dev, (T, k), torch.float32)
+            dtopk_w = _new(stream, dout_perm, (T, k), torch.float32)
         if scratch is None:
-            scratch = _new(stream, dev, need, torch.uint8)
+            scratch = _new(stream, dout_perm, need, torch.uint8)
     _run("moe_grouped_dgrad_swiglu_ckpt8", stream, ("dout_perm", dout_perm), ("offsets", offsets),
          ("counts", counts), ("tile_expert", tile_expert), E, D, F, m_tile, m_cap, ("w2", w2),
          ("ab_codes", ab_codes), ("ab_scales", ab_scales), ("src_row", src_row),
