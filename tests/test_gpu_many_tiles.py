@@ -87,7 +87,7 @@ def edges(t, tok, used, poison):
 @pytest.mark.parametrize("name,split", cases(CKPT))
 def test_save(name, split):
     counts, mt, D, F = CKPT[name]
-    P.log(f"[rounds] save {name} split={split}")
+    P.log(f"[tiles] save {name} split={split}")
     torch.manual_seed(51)
     offs, do, te, m_cap, tok, cnt = setup(counts, mt)
     x = torch.randn((m_cap, D), **BF)
@@ -119,7 +119,7 @@ def test_save(name, split):
 @pytest.mark.parametrize("name,split", cases(CKPT))
 def test_use(name, split):
     counts, mt, D, F = CKPT[name]
-    P.log(f"[rounds] use {name} split={split}")
+    P.log(f"[tiles] use {name} split={split}")
     torch.manual_seed(52)
     offs, do, te, m_cap, tok, cnt = setup(counts, mt)
     used, k = int(offs[-1]), 2
@@ -169,7 +169,7 @@ def test_use(name, split):
 @pytest.mark.parametrize("name,split", cases(MX4))
 def test_products(name, fc, split):
     counts, mt, K, N = MX4[name]
-    P.log(f"[rounds] 4-bit fc{fc} {name} split={split}")
+    P.log(f"[tiles] 4-bit fc{fc} {name} split={split}")
     torch.manual_seed(53)
     offs, do, te, m_cap, tok, cnt = setup(counts, mt)
     used, E = int(offs[-1]), len(counts)
