@@ -28,6 +28,11 @@ namespace moe {
 namespace {
 
 constexpr int kParts = 256;      // most rows of partial sums
+// Most workgroups of the forward; longer batches take several turns of each. One for every few tokens
+// would pass the 2^32 threads of a launch from 2^26 tokens, of which the runtime then keeps the low 32
+// bits. Far fewer are slower: each turn begins with its loads (65536 x 4096, top-4: 656 us, 64
+// workgroups a CU 709; 262144 x 1024: 667 and 724).
+constexpr int kMostGroups = 1 << 21;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -395,7 +400,8 @@ int launch_bwd(const BorderBwdCall& c, hipStream_t s) {
 template <typename TIn, int VC, int WPB, int kJ>
 void launch_vc(const BorderCall& c, hipStream_t s) {
   const int G = waves_for(c.D, VC), tpb = WPB / G;
-  hipLaunchKernelGGL((border_kernel<TIn, VC, WPB, kJ>), dim3((c.T + tpb - 1) / tpb), dim3(WPB * 64), 0, s, c, G);
+  const int n = std::min(kMostGroups, (c.T + tpb - 1) / tpb);
+  hipLaunchKernelGGL((border_kernel<TIn, VC, WPB, kJ>), dim3(n), dim3(WPB * 64), 0, s, c, G);
 }
 
 template <typename TIn>
