@@ -35,6 +35,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTok = 32;       // tokens of a workgroup of the first kernel, and T's padding
 constexpr int kDlWaves = 16;
+// Most workgroups of the first kernel along the grid's x, the others along its y: one for every kTok tokens
+// along x alone would pass the 2^32 threads of that dimension from 2^27 tokens, of which the runtime then
+// keeps the low 32 bits. (Turns of fewer workgroups instead: 65536 tokens over 64 experts 43.8 us against 41.6.)
+constexpr int kMostX = 1 << 16;
 constexpr int kShort = 1024;   // tokens of a short batch
 constexpr int kWaves = 8;          // waves of a workgroup of the products
 constexpr int kDxWaves = 2048;     // and dx
@@ -198,7 +202,9 @@ __global__ __launch_bounds__(kDlWaves * 64) void route_dl_kernel(const RouteBwdC
   constexpr int R = NE == 16 ? 1 : kTok / kDlWaves, W = kDlWaves;
   __shared__ float tile[kTok * (64 * NE + 1)];   // [kTok][Ep + 1]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.x * kTok, ld = Ep + 1;
+  const int group = blockIdx.y * gridDim.x + blockIdx.x;
+  if (group >= Tp / kTok) return;
+  const int t0 = group * kTok, ld = Ep + 1;
   for (int r = wave; r < kTok; r += W)
     for (int e = a.E + lane; e < Ep; e += 64) tile[r * ld + e] = 0.0f;
   for (int r = wave; r < kTok; r += W * R) token_dl<NE, R>(a, t0 + r, W, lane, tile + r * ld, ld);
@@ -232,7 +238,7 @@ __global__ __launch_bounds__(kDlWaves * 64) void route_dl_kernel(const RouteBwdC
     const int r = 4 * (lane & 7);
     for (int e = wave * 8 + (lane >> 3); e < Ep; e += 8 * W) {
       const float* v = tile + r * ld + e;
-      put(p.cols, ((size_t)blockIdx.x * Ep + e) * kTok + r, ncol, {v[0], v[ld], v[2 * ld], v[3 * ld]},
+      put(p.cols, ((size_t)group * Ep + e) * kTok + r, ncol, {v[0], v[ld], v[2 * ld], v[3 * ld]},
           std::integral_constant<int, SP>());
     }
   }
@@ -240,7 +246,7 @@ __global__ __launch_bounds__(kDlWaves * 64) void route_dl_kernel(const RouteBwdC
     for (int e = threadIdx.x; e < a.E; e += W * 64) {
       float s = 0.0f;
       for (int r = 0; r < kTok; ++r) s += tile[r * ld + e];
-      p.dbias[(size_t)blockIdx.x * a.E + e] = s;
+      p.dbias[(size_t)group * a.E + e] = s;
     }
 }
 
@@ -544,7 +550,8 @@ hipError_t launch_typed(const RouteBwdCall& c, hipStream_t s) {
   const auto dl = c.E <= 64    ? route_dl_kernel<TIn, 1>
                   : c.E <= 128 ? route_dl_kernel<TIn, 2>
                                : (c.E <= 256 ? route_dl_kernel<TIn, 4> : route_dl_kernel<TIn, 16>);
-  hipLaunchKernelGGL(dl, dim3(groups), dim3(kDlWaves * 64), 0, s, c, w, p.Ep, p.Tp);
+  const int gx = std::min(groups, kMostX);
+  hipLaunchKernelGGL(dl, dim3(gx, (groups + gx - 1) / gx), dim3(kDlWaves * 64), 0, s, c, w, p.Ep, p.Tp);
   const int blocks16 = (c.T + 15) / 16;
   const int per = std::max<int>(1, (int)(((int64_t)blocks16 * p.strips + kDxWaves - 1) / kDxWaves));
   const int64_t dxw = p.Ep <= 64 ? (int64_t)((blocks16 + per - 1) / per) * p.strips
