@@ -17,6 +17,10 @@ constexpr int kHistTokens = 256;
 // Largest top-k the entry points accept.
 constexpr int kMaxTopK = 32;
 
+// Tokens of one launch that has up to 64 threads a token: a dimension of a launch holds fewer than 2^32
+// threads, and the runtime keeps the low 32 bits of more without an error.
+constexpr int kLaunchTokens = 1 << 25;
+
 int cu_count();  // compute units of the current device (cached per device)
 
 hipError_t launch_route(int dt, const void* x, const void* wg, const float* bias, int T, int D,

@@ -20,6 +20,7 @@
 // and the top-k choice is reproducible bit for bit. In the softmax and top-k each lane
 // holds the logits of experts lane, lane + 64, ... (up to 16 of them: 1024 experts);
 // each top-k round takes every lane's best available expert, then the wave's.
+#include <algorithm>
 #include <math.h>
 
 #include "common.hpp"
@@ -191,12 +192,17 @@ void launch_typed(const TIn* x, const TIn* wg, const float* bias, int T, int D, 
 hipError_t launch_route(int dt, const void* x, const void* wg, const float* bias, int T, int D,
                         int E, int k, int renorm, int32_t* topk_idx, float* topk_w, float* logits,
                         hipStream_t s) {
-  if (dt == kF32)
-    launch_typed(static_cast<const float*>(x), static_cast<const float*>(wg), bias, T, D, E, k,
-                 renorm, topk_idx, topk_w, logits, s);
-  else
-    launch_typed(static_cast<const bf16_t*>(x), static_cast<const bf16_t*>(wg), bias, T, D, E, k,
-                 renorm, topk_idx, topk_w, logits, s);
+  for (int t0 = 0; t0 < T; t0 += kLaunchTokens) {   // tokens do not depend on each other
+    const int n = std::min(kLaunchTokens, T - t0);
+    const size_t at = (size_t)t0 * D, slot = (size_t)t0 * k;
+    float* lg = logits ? logits + (size_t)t0 * E : nullptr;
+    if (dt == kF32)
+      launch_typed(static_cast<const float*>(x) + at, static_cast<const float*>(wg), bias, n, D, E,
+                   k, renorm, topk_idx + slot, topk_w + slot, lg, s);
+    else
+      launch_typed(static_cast<const bf16_t*>(x) + at, static_cast<const bf16_t*>(wg), bias, n, D,
+                   E, k, renorm, topk_idx + slot, topk_w + slot, lg, s);
+  }
   return hipGetLastError();
 }
 
