@@ -870,9 +870,10 @@ hipError_t launch_permute(int dt, const void* x, const int32_t* topk_idx, int T,
   const int ngroups = (T + kCopyTokens - 1) / kCopyTokens;
   // rank and copy in one launch while every workgroup reading the whole table stays cheap
   // (at most 2^24 table reads in all: e.g. 16384 tokens with 64 experts), or reads two
-  // rows of the prefix-summed table
+  // rows of the prefix-summed table, and a workgroup for every group of tokens stays within the
+  // threads of a launch
   const bool scanned = scan_hist(hist, nbh, E, s);
-  if (scanned || (int64_t)ngroups * nbh * E <= ((int64_t)1 << 24)) {
+  if ((scanned || (int64_t)ngroups * nbh * E <= ((int64_t)1 << 24)) && T <= kLaunchTokens) {
     if (dt == kF32)
       hipLaunchKernelGGL(place_kernel<float>, dim3(ngroups), dim3(kThreads), 0, s,
                          static_cast<const float*>(x), topk_idx, T, D, k, E, m_tile, m_cap, nbh,

@@ -38,3 +38,25 @@ def test_route(T, E, k):
     want = rpg.moe_route(base, wg, k, want_logits=True)
     for got, one in zip(rpg.moe_route(x, wg, k, want_logits=True), want):
         same(got, one)
+
+
+@pytest.mark.parametrize("T", [1 << 26, (1 << 26) + 5])
+def test_permute_and_combine(T):
+    E, mt = 3, 16
+    base, x = rows(T)
+    idx = (torch.arange(T, device="cuda") % 7 % 4).to(torch.int32)[:, None].contiguous()
+    idx[idx == 3] = -1
+    p = rpg.moe_permute(x, idx, E, mt)
+    counts = torch.stack([(idx == e).sum() for e in range(E)])
+    seg = (counts + mt - 1) // mt * mt
+    start = torch.cumsum(seg, 0) - seg
+    assert torch.equal(p["counts"].long(), counts) and torch.equal(p["offsets"][:E].long(), start) and int(p["dev_err"]) == 0
+    dst = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    for e in range(E):
+        at = (idx[:, 0] == e).nonzero()[:, 0]
+        dst[at] = (start[e] + torch.arange(at.numel(), device="cuda")).to(torch.int32)
+        assert torch.equal(p["src_row"][start[e]:start[e] + counts[e]].long(), at)
+        assert torch.equal(p["x_perm"][start[e]:start[e] + counts[e]], x[at])
+        assert not bool(p["x_perm"][start[e] + counts[e]:start[e] + seg[e]].any())
+        del at
+    assert torch.equal(p["dst_row"][:, 0], dst)
