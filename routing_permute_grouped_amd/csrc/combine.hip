@@ -16,6 +16,7 @@
 // gradient <dout[t], y_perm[row]> is reduced by the row's wave in a fixed order; pad
 // rows get zeros, so the grouped GEMMs of the backward see exact zeros there.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "kernels.hpp"
@@ -198,16 +199,21 @@ hipError_t launch_combine(int dt, const void* y_perm, const int32_t* dst_row, co
   // tokens per workgroup: up to kTokens, fewer when that leaves the grid too small
   int tpb = kTokens;
   while (tpb > 1 && (T + tpb - 1) / tpb < 8 * cu_count()) tpb >>= 1;
-  const dim3 grid((T + tpb - 1) / tpb), block(kThreads);
+  const dim3 block(kThreads);
+  auto launch = [&](auto* y, auto* sh, auto* o) {
+    for (int t0 = 0; t0 < T; t0 += kLaunchTokens) {   // tokens do not depend on each other
+      const int n = std::min(kLaunchTokens, T - t0);
+      const size_t at = (size_t)t0 * D, slot = (size_t)t0 * k;
+      const auto kernel = combine_kernel<std::remove_pointer_t<decltype(o)>>;
+      hipLaunchKernelGGL(kernel, dim3((n + tpb - 1) / tpb), block, 0, s, y, dst_row + slot,
+                         topk_w ? topk_w + slot : nullptr, sh ? sh + at : nullptr, n, D, k, m_cap, tpb,
+                         o + at);
+    }
+  };
   if (dt == kF32)
-    hipLaunchKernelGGL(combine_kernel<float>, grid, block, 0, s, static_cast<const float*>(y_perm),
-                       dst_row, topk_w, static_cast<const float*>(shared), T, D, k, m_cap, tpb,
-                       static_cast<float*>(out));
+    launch(static_cast<const float*>(y_perm), static_cast<const float*>(shared), static_cast<float*>(out));
   else
-    hipLaunchKernelGGL(combine_kernel<bf16_t>, grid, block, 0, s,
-                       static_cast<const bf16_t*>(y_perm), dst_row, topk_w,
-                       static_cast<const bf16_t*>(shared), T, D, k, m_cap, tpb,
-                       static_cast<bf16_t*>(out));
+    launch(static_cast<const bf16_t*>(y_perm), static_cast<const bf16_t*>(shared), static_cast<bf16_t*>(out));
   return hipGetLastError();
 }
 

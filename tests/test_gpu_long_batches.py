@@ -60,3 +60,11 @@ def test_permute_and_combine(T):
         assert not bool(p["x_perm"][start[e] + counts[e]:start[e] + seg[e]].any())
         del at
     assert torch.equal(p["dst_row"][:, 0], dst)
+    # combine takes the rows back, weighted
+    w = torch.full((T, 1), 0.5, device="cuda")
+    out = rpg.moe_combine(p["x_perm"], p["dst_row"], w, shared=x, m_cap=p["m_cap"])
+    gone = dst < 0
+    assert torch.equal(out[gone], x[gone])
+    # half of a value is exact, the sum with the shared row is rounded once
+    one = (base.float() * 0.5 + base.float()).to(torch.bfloat16)
+    assert bool(torch.where(gone[:, None], True, out == long(one, T)).all())
