@@ -85,7 +85,8 @@ size_t moe_layer_few_workspace_bytes(moe_dtype_t dt, int T, int k, int F, int Fs
  *   y_perm NULL: u = shared (T rows a caller has already, then needed); shared [T,D] or NULL;
  *   gate [T] float32 or NULL; gamma_post, gamma_next [D] (dt) or NULL
  *   -> out [T,D], x_next [T,D] (needed with gamma_next), and, each where not NULL, u [T,D] (dt),
- *      rstd_post [T], rstd_next [T] float32: what the backward reads.
+ *      rstd_post [T], rstd_next [T] float32: what the backward reads. rstd_post is only taken with
+ *      gamma_post, x_next and rstd_next only with gamma_next (else MOE_EINVAL).
  * Float32 between the reads and one rounding of each result (x_next is of out before its
  * rounding, z of u before its). Slots whose dst_row is outside [0, m_cap) are skipped. out may
  * be resid's buffer (in place); no other buffers may overlap.

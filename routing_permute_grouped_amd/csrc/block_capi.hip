@@ -104,7 +104,9 @@ moe_status_t moe_combine_norm(moe_dtype_t dt, const void* resid, const void* y_p
     return MOE_EINVAL;
   if (y_perm ? !aligned16(y_perm) || !aligned4(dst_row) || !opt4(topk_w) : !shared)
     return MOE_EINVAL;
-  if (gamma_next && !aligned16(x_next)) return MOE_EINVAL;
+  // a result that no norm writes is refused, not left as it was
+  if (gamma_next ? !aligned16(x_next) : x_next || rstd_next) return MOE_EINVAL;
+  if (!gamma_post && rstd_post) return MOE_EINVAL;
   if (!norm_sizes_ok(T, D)) return MOE_ESHAPE;
   if (y_perm) {
     if (!tk_ok(T, k) || k < 1 || k > kMaxK) return MOE_ESHAPE;

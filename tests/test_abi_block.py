@@ -142,6 +142,13 @@ def test_combine_norm_validates(kw, code):
     assert combine(**kw) == code
 
 
+@pytest.mark.parametrize("kw", [dict(gp=None, rp=FAKE), dict(gn=None, xn=None, rn=FAKE), dict(gn=None), dict(gp=None, gn=None, xn=None, rp=FAKE)])
+def test_combine_norm_refuses_results_of_a_norm_it_does_not_take(kw):
+    # sizes that are refused as well: a call that passes these checks launches nothing here
+    assert combine(T=0, gp=None, gn=None, xn=None) == combine(T=0, rp=FAKE, rn=FAKE) == MOE_ESHAPE
+    assert combine(T=0, **kw) == MOE_EINVAL
+
+
 def combine_bwd(dt=1, dout=FAKE, dx=FAKE, u=FAKE, out=FAKE, gate=None, gp=FAKE, gn=FAKE, rp=FAKE, rn=FAKE, scale=1.0, T=4, D=128, du=FAKE, dr=FAKE,
                 dgate=None, dgp=FAKE, dgn=FAKE, ws=FAKE, n=1 << 30):
     return lib.moe_combine_norm_backward(dt, dout, dx, u, out, gate, gp, gn, rp, rn, scale, T, D, du, dr, dgate, dgp, dgn, ws, n, None)
