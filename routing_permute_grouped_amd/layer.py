@@ -480,6 +480,8 @@ def moe_block_backward(fwd: dict, dout: Optional[torch.Tensor], resid: torch.Ten
     res.update(K.moe_route_backward(res["dtopk_w"], fwd["topk_idx"], fwd["logits"], x, wg,
                                     renorm=renorm, dlogits_add=dlogits_add, dx_add=res["dx"]))
     res.update(bb)
+    if gamma_next is not None and dx_next is None:   # nothing came through that norm
+        res["dgamma_next"] = torch.zeros(gamma_next.shape, dtype=torch.float32, device=x.device)
     if gamma_pre is not None:
         res["dresid"], res["dgamma_pre"] = K.moe_norm_backward(res["dx"], resid, gamma_pre,
                                                                fwd["rstd_pre"],
