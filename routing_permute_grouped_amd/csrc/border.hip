@@ -433,9 +433,12 @@ hipError_t launch_border(int dt, const BorderCall& c, hipStream_t s) {
 size_t border_workspace_bytes(int T, int D) { return (size_t)2 * parts_of(T) * D * sizeof(float); }
 
 hipError_t launch_border_backward(int dt, const BorderBwdCall& c, hipStream_t s) {
-  // 8 waves of 16 (float32: 8) values a lane leave the registers for the loads ahead. From D = 4096
-  // 16 waves of 8 values keep more loads on the way (16384 x 4096: 134.8 against 139.4 us; 16384 x
-  // 1024: 42.6 against 39.9); a wider row takes all the registers of 16 waves.
+  // bf16: 8 waves of 16 values a lane, from D = 4096 16 waves of 8, which keep more loads on the way
+  // (16384 tokens, us: D = 1024 40.4 against 43.9, 2048 75 both, 2880 108.7 against 104.2, 4096 137.3
+  // against 134.7, 5120 204.6 against 202.6; 8192 x 7168 126.3 against 129.4). float32: 8 waves of 8 values.
+  // Wider rows take 16 waves of 16 values, at most 128 registers each, without loads ahead: bf16 past D =
+  // 8192 spills 52 registers (8192 x 16384: 526 us, 3.1 TB/s), float32 past 4096 87 (8192 x 7168: 375 us, 3.8
+  // TB/s; 8192 x 4096, which does not, 133 us, 6.1).
   int n;
   if (dt == kF32)
     n = c.D <= 4096 ? launch_bwd<float, 8, 8, true>(c, s) : launch_bwd<float, 16, 16, false>(c, s);

@@ -664,6 +664,9 @@ __device__ __forceinline__ void fc2_units(const FewArgs& a, const Tables& tb, in
 template <int W, int S, int NS, bool HL>
 __global__ __launch_bounds__(THREADS) void few_fc2(const FewArgs a) {
   typedef typename Fmt<W>::Act Act;
+  // units in flight. They matter where rows of h come from the L2 (16 tokens over 8 experts of 14336, the
+  // call in us: bf16 2 506, 3 482, 4 502; 32 tokens, 4 bits: 1 254, 2 251, 3 249, 4 251); with h in LDS one
+  // token over 64 experts takes 40 to 41 with one to four, 4-bit 27.7 with two or three, 28.6 with four or six
   constexpr int PW = W == kFewMx4 ? (HL ? 4 : 2) : (HL ? 2 : 3), PS = 2, RC = 16 / NS;
   __shared__ Tables tb;
   __shared__ __attribute__((aligned(256))) char pool[HL ? POOL : MAXT * 1024];
@@ -772,7 +775,9 @@ void launch_fmt(FewArgs a, hipStream_t s) {
 template <typename TIn>
 void launch_logits(const FewArgs& a, hipStream_t s) {
   // a token at a time where that does not fill the card (8 tokens, 256 experts of D = 7168: the call
-  // 143.5 us, four at a time 148)
+  // 143.5 us, four at a time 148; calls with F = 128 and top-1, one at a time against four: 12 tokens over
+  // these 41 and 43.5, 16 46 and 48, 24 50 both, 32 58 and 57.5; over 8 experts of 4096 12 tokens 23.8 and 25.9,
+  // 24 25.5 and 27.7, 32 26.1 and 28.3)
   const bool one = a.T < 16;
   const auto f = one ? few_logits<TIn, 1> : few_logits<TIn, 4>;
   const dim3 grid((a.E + LOGIT_WAVES - 1) / LOGIT_WAVES, one ? a.T : (a.T + 3) / 4);

@@ -498,7 +498,9 @@ def moe_block_few(resid: torch.Tensor, weights, k: int, wg: torch.Tensor,
                   renorm: bool = False) -> dict:
     """moe_block for the at most 32 tokens of a decode step: the layer is moe_layer_few, or with
     ``weights`` an Mx4Weights moe_layer_few_mxfp4 (else ``weights`` is (w1, w3, w2)). Returns
-    out, x_next, topk_idx and topk_w."""
+    out, x_next, topk_idx and topk_w. From about 8 tokens over wide 4-bit experts
+    moe_layer_masked_mxfp4 between moe_norm and moe_combine_norm (its out as ``shared``) is faster:
+    8 experts of D = 4096, F = 14336, top-2, 32 tokens 167 us a layer against 251."""
     if (x is None) == (gamma_pre is None):
         raise ValueError("x or gamma_pre, one of the two")
     if x is None:
